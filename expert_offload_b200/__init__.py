@@ -25,8 +25,13 @@ STATUS = {0: "HFQ_OK", -1: "HFQ_ERR_ARG", -2: "HFQ_ERR_ALIGN", -3: "HFQ_ERR_UNSU
 HFQ_F32, HFQ_BF16 = 0, 1
 PATH_AUTO, PATH_GEMV, PATH_TC = 0, 1, 2
 ARENA_HUGEPAGE = 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GATE_NONE, GATE_TOKEN, GATE_CHANNEL, GATE_FULL = 0, 1, 2, 3
+GATE_LINEAR, GATE_SIGMOID = 0, 1
+ACT_NONE, ACT_SWIGLU = 0, 1
 BLOCK, BLOCK_BYTES = 256, 136
 MAX_EXPERTS, MAX_TOPK, MAX_STACK_LAYERS = 512, 16, 64
+MAX_GROUPS, Q8_MAX_K = 32, 16384
 
 
 class HfqError(RuntimeError):
@@ -39,6 +44,17 @@ class HfqError(RuntimeError):
 class hfq4_layer(ctypes.Structure):
     _fields_ = [("expert_ptr", ctypes.c_void_p), ("expert_loc", ctypes.c_void_p),
                 ("n_experts", ctypes.c_int), ("hidden", ctypes.c_int), ("inter", ctypes.c_int)]
+
+
+class moe_route_rule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int), ("n_groups", ctypes.c_int), ("topk_groups", ctypes.c_int),
+                ("group_top", ctypes.c_int), ("renormalise", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class moe_norm_rule(ctypes.Structure):
+    _fields_ = [("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p), ("w_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("w_offset", ctypes.c_float), ("residual_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("gate_kind", ctypes.c_int), ("gate_act", ctypes.c_int)]
 
 
 _vp, _i, _sz, _u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64
@@ -54,6 +70,15 @@ _SIGS = {
     "hfq4_dequant": (_i, [_vp, _i, _i, _vp, _vp]),
     "hfq_route_workspace_bytes": (_sz, [_i, _i, _i]),
     "moe_route": (_i, [_vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_route_scored_workspace_bytes": (_sz, [_i, _i, _i]),
+    "moe_route_scored": (_i, [_vp, _i, _i, _i, _i, _vp, ctypes.POINTER(moe_route_rule), _i, _vp, _vp, _vp,
+                              _vp, _vp, _vp, _sz, _vp]),
+    "moe_norm_residual": (_i, [ctypes.POINTER(moe_norm_rule), _i, _i, _vp, _i, _i, _vp, _vp, _i, _i, _vp,
+                               _vp, _vp, _vp, _i, _vp, _vp, _vp]),
+    "q8_quantize_rows": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _i, _vp, _vp]),
+    "q8_matmul": (_i, [_vp, _i, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _i, _i, _vp]),
+    "q8_linear_workspace_bytes": (_sz, [_i, _i, _i]),
+    "q8_linear": (_i, [_vp, _i, _i, _i, _i, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _sz, _vp]),
     "hfq4_moe_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "hfq4_moe_forward": (_i, [ctypes.POINTER(hfq4_layer), _vp, _i, _i, _vp, _vp, _i, _vp, _vp,
                               _vp, _vp, _vp, _i, _vp, _sz, _vp]),
@@ -134,6 +159,39 @@ def _nbytes(a) -> int:
     return int(a.numel() * a.element_size())
 
 
+_I32, _I8 = 16, 17                       # operand types besides HFQ_F32 and HFQ_BF16
+_types = {}
+
+
+def _operands(*ops) -> None:
+    """Checks the operands (name, tensor, type, elements): a CUDA tensor of the
+    current device (whose stream the call goes to), of that type (None: any),
+    its last dimension dense, with at least that many elements behind its
+    address; or a raw device address, which is the caller's word."""
+    torch = sys.modules.get("torch")
+    if torch is not None and not _types:
+        _types.update({HFQ_F32: (torch.float32,), HFQ_BF16: (torch.bfloat16, torch.int16, torch.uint16),
+                       _I32: (torch.int32,), _I8: (torch.int8,)})
+    device = None
+    for name, t, kind, n in ops:
+        if t is None or isinstance(t, int):
+            continue
+        if torch is None or not isinstance(t, torch.Tensor):
+            raise HfqError(-1, f"{name} is neither a CUDA tensor nor a device address")
+        if device is None:
+            device = torch.cuda.current_device() if torch.cuda.is_available() else None
+        if not t.is_cuda or t.get_device() != device:
+            raise HfqError(-1, f"{name} is on {t.device}, not on the current CUDA device")
+        if kind is None:
+            continue
+        if t.dtype not in _types.get(kind, ()):
+            raise HfqError(-1, f"{name} is {t.dtype}, which is not the type the call names")
+        if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise HfqError(-1, f"{name}: the elements of a row are not next to each other")
+        if t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < n:
+            raise HfqError(-1, f"{name} holds fewer than the {n} elements the call reads or writes")
+
+
 def _stream(s):
     if s is None:
         torch = sys.modules.get("torch")
@@ -191,6 +249,102 @@ def moe_router_logits(x, x_dtype: int, T: int, hidden: int, router, router_dtype
     """logits [T, E] f32 = x Wr^T on the device."""
     _check(lib().moe_router_logits(_ptr(x), x_dtype, T, hidden, _ptr(router), router_dtype,
                                    n_experts, _ptr(logits), _stream(stream)))
+
+
+class RouteRule:
+    """How moe_route_scored scores, groups and weighs (a moe_route_rule)."""
+
+    def __init__(self, score: int = SCORE_SOFTMAX, n_groups: int = 1, topk_groups: int = 1,
+                 group_top: int = 1, renormalise: bool = True, scale: float = 1.0):
+        self.struct = moe_route_rule(score, n_groups, topk_groups, group_top, int(renormalise), scale)
+
+
+def moe_route_scored_workspace_bytes(T: int, E: int, k: int) -> int:
+    return lib().moe_route_scored_workspace_bytes(T, E, k)
+
+
+def moe_route_scored(logits, logits_dtype: int, T: int, E: int, k: int, rule: RouteRule, idx, wts,
+                     bias=None, cnt=None, off=None, perm=None, workspace=None, ld: int = 0,
+                     stream=None) -> None:
+    """Top-k routing by scores and a bias, with groups; lists as moe_route's."""
+    _operands(("logits", logits, logits_dtype, (T - 1) * (ld or E) + E), ("bias", bias, HFQ_F32, E),
+              ("idx", idx, _I32, T * k), ("wts", wts, HFQ_F32, T * k), ("cnt", cnt, _I32, E),
+              ("off", off, _I32, E + 1), ("perm", perm, _I32, T * k), ("workspace", workspace, None, 0))
+    ws_bytes = _nbytes(workspace) if workspace is not None else 0
+    _check(lib().moe_route_scored(_ptr(logits), logits_dtype, ld, T, E, _ptr(bias),
+                                  ctypes.byref(rule.struct), k, _ptr(idx), _ptr(wts), _ptr(cnt),
+                                  _ptr(off), _ptr(perm), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+# ---------------------------------------------------- norm, gate, residual
+
+class NormRule:
+    """What moe_norm_residual does to every row (a moe_norm_rule); keeps the
+    weights it points to alive."""
+
+    def __init__(self, w_post=None, w_pre=None, w_dtype: int = HFQ_BF16, eps: float = 1e-6,
+                 w_offset: float = 0.0, residual_scale: float = 1.0, branch_scale: float = 1.0,
+                 gate_kind: int = GATE_NONE, gate_act: int = GATE_LINEAR):
+        self.w_post, self.w_pre = w_post, w_pre
+        self.struct = moe_norm_rule(_ptr(w_post), _ptr(w_pre), w_dtype, eps, w_offset, residual_scale,
+                                    branch_scale, gate_kind, gate_act)
+
+
+def moe_norm_residual(rule: NormRule, T: int, H: int, x, x_dtype: int, y=None, y_dtype: int = HFQ_F32,
+                      y2=None, y2_gate=None, gate=None, x_out=None, xn=None, xn_dtype: int = HFQ_BF16,
+                      xq=None, xq_scale=None, ldx: int = 0, ldy: int = 0, stream=None) -> None:
+    """x' = residual_scale x + branch_scale gate norm(y + y2), xn = norm(x')."""
+    st = rule.struct
+    nx, ny = (T - 1) * (ldx or H) + H, (T - 1) * (ldy or H) + H
+    _operands(("x", x, x_dtype, nx), ("y", y, y_dtype, ny), ("y2", y2, y_dtype, ny),
+              ("y2_gate", y2_gate, HFQ_F32, T),
+              ("gate", gate, HFQ_F32, {GATE_TOKEN: T, GATE_CHANNEL: H, GATE_FULL: T * H}.get(st.gate_kind, 0)),
+              ("x_out", x_out, x_dtype, nx), ("xn", xn, xn_dtype, T * H),
+              ("xq", xq, _I8, T * (-(-H // 16) * 16)), ("xq_scale", xq_scale, HFQ_F32, T),
+              ("w_post", rule.w_post, st.w_dtype, H), ("w_pre", rule.w_pre, st.w_dtype, H))
+    _check(lib().moe_norm_residual(ctypes.byref(st), T, H, _ptr(x), x_dtype, ldx, _ptr(y), _ptr(y2),
+                                   y_dtype, ldy, _ptr(y2_gate), _ptr(gate), _ptr(x_out), _ptr(xn),
+                                   xn_dtype, _ptr(xq), _ptr(xq_scale), _stream(stream)))
+
+
+# --------------------------------------------------- products in 8 bits
+
+def q8_quantize_rows(x, x_dtype: int, rows: int, cols: int, q, scale, act: int = ACT_NONE, ldx: int = 0,
+                     ldq: int = 0, stream=None) -> None:
+    """int8 rows and their f32 scales; act ACT_SWIGLU quantises silu(gate) * up."""
+    width = 2 * cols if act == ACT_SWIGLU else cols
+    c16 = -(-cols // 16) * 16
+    _operands(("x", x, x_dtype, (rows - 1) * (ldx or width) + width),
+              ("q", q, _I8, (rows - 1) * (ldq or c16) + c16), ("scale", scale, HFQ_F32, rows))
+    _check(lib().q8_quantize_rows(_ptr(x), x_dtype, ldx, rows, cols, act, _ptr(q), ldq, _ptr(scale),
+                                  _stream(stream)))
+
+
+def q8_matmul(xq, xs, T: int, K: int, wq, ws, N: int, y, y_dtype: int, ldxq: int = 0, ldw: int = 0,
+              ldy: int = 0, stream=None) -> None:
+    """y = (xq wq^T) * xs * ws for quantised rows xq and channels wq."""
+    k16 = -(-K // 16) * 16
+    _operands(("xq", xq, _I8, (T - 1) * (ldxq or k16) + k16), ("xs", xs, HFQ_F32, T),
+              ("wq", wq, _I8, (N - 1) * (ldw or k16) + k16), ("ws", ws, HFQ_F32, N),
+              ("y", y, y_dtype, (T - 1) * (ldy or N) + N))
+    _check(lib().q8_matmul(_ptr(xq), ldxq, _ptr(xs), T, K, _ptr(wq), ldw, _ptr(ws), N, _ptr(y), y_dtype, ldy,
+                           _stream(stream)))
+
+
+def q8_linear_workspace_bytes(T: int, K: int, N: int) -> int:
+    return lib().q8_linear_workspace_bytes(T, K, N)
+
+
+def q8_linear(x, x_dtype: int, T: int, K: int, wq, ws, N: int, y, y_dtype: int, workspace=None, ldx: int = 0,
+              ldw: int = 0, ldy: int = 0, stream=None) -> None:
+    """y = x W^T with x quantised on the way: q8_quantize_rows, then q8_matmul."""
+    k16 = -(-K // 16) * 16
+    _operands(("x", x, x_dtype, (T - 1) * (ldx or K) + K), ("wq", wq, _I8, (N - 1) * (ldw or k16) + k16),
+              ("ws", ws, HFQ_F32, N), ("y", y, y_dtype, (T - 1) * (ldy or N) + N),
+              ("workspace", workspace, None, 0))
+    ws_bytes = _nbytes(workspace) if workspace is not None else 0
+    _check(lib().q8_linear(_ptr(x), x_dtype, ldx, T, K, _ptr(wq), ldw, _ptr(ws), N, _ptr(y), y_dtype, ldy,
+                           _ptr(workspace), ws_bytes, _stream(stream)))
 
 
 # ---------------------------------------------------------------- forward

@@ -166,6 +166,164 @@ hfq_status moe_router_logits(const void *x, hfq_dtype x_dtype, int T, int hidden
                              hfq_dtype router_dtype, int n_experts, float *logits, void *stream);
 
 /*
+ * Scored top-k routing (device): moe_route with a choice of score, a bias
+ * that balances the experts, groups of experts, and scaled weights.
+ *   Per token, with l its logits and b the bias (0 without one):
+ *     s_e = softmax(l)_e (HFQ_SCORE_SOFTMAX) or 1 / (1 + exp(-l_e)) (SIGMOID);
+ *     c_e = s_e + b_e, which decides the selection and nothing else;
+ *     groups are runs of n_experts / n_groups experts; a group's score is the
+ *     sum of its group_top best c (1 or 2), and only the topk_groups best
+ *     groups (ties to the lower group) stay;
+ *     idx = the k experts of those groups with the largest c, slot 0 the
+ *     largest, equal ones to the lower expert;
+ *     wts_j = s_j * scale, or s_j / (sum of the selected s) * scale with
+ *     renormalise.
+ *   c and the group scores are compared as 64-bit values, so that the
+ *   selection does not hang on a rounding: where 32 bits decide, they are
+ *   used, and where two candidates lie within their error the token is
+ *   decided again in 64 (without a bias the logits themselves are compared).
+ *   Masked experts: a logit of -inf or NaN, or a bias of -inf or NaN, takes
+ *   an expert out.  Its score is 0 and it is no member of its group's sum; it
+ *   ranks behind all others of its group's standing (among masked ones the
+ *   lower index first) and, where it is selected for want of others, weighs 0.
+ *   A group without a live expert ranks last.  A logit of +inf counts as the
+ *   largest finite f32.  A token whose experts are all masked gets the first k
+ *   experts and weights of 0; so do renormalised weights that sum to 0.
+ *   logits:  [T][n_experts] in logits_dtype, rows ld elements apart (0 =
+ *            n_experts; else ld >= n_experts), aligned to their type.
+ *   bias:    f32 [n_experts] or NULL.
+ *   idx, wts, cnt, off, perm, workspace: as for moe_route;
+ *            moe_route_scored_workspace_bytes(T, E, k) bytes, 16-byte
+ *            aligned, needed only with the lists (it may be NULL when that
+ *            is 0), with no state kept between calls.  Calls that share a
+ *            workspace must be ordered.
+ *   Limits: n_groups <= 32 and divides n_experts; 1 <= topk_groups <=
+ *            n_groups; group_top 1 or 2 and <= n_experts / n_groups;
+ *            k <= topk_groups * n_experts / n_groups; scale finite.
+ */
+#define HFQ_SCORE_SOFTMAX 0
+#define HFQ_SCORE_SIGMOID 1
+#define HFQ_MAX_GROUPS 32
+typedef struct {
+    int score;         /* HFQ_SCORE_SOFTMAX or HFQ_SCORE_SIGMOID */
+    int n_groups;      /* 1: no groups */
+    int topk_groups;
+    int group_top;
+    int renormalise;   /* 0 or 1 */
+    float scale;
+} moe_route_rule;
+size_t moe_route_scored_workspace_bytes(int T, int E, int k);
+hfq_status moe_route_scored(const void *logits, hfq_dtype logits_dtype, int ld, int T, int E,
+                            const float *bias, const moe_route_rule *rule, int k, int32_t *idx,
+                            float *wts, int32_t *cnt, int32_t *off, int32_t *perm, void *workspace,
+                            size_t ws_bytes, void *stream);
+
+/*
+ * The norms around a block, with its gate and the residual scale (device),
+ * one pass over the data:
+ *     b   = y + sigmoid(y2_gate[t]) * y2           (y2 NULL: b = y; y2_gate
+ *                                                   NULL: b = y + y2)
+ *     b   = b * rsqrt(mean(b^2) + eps) * (w_post + w_offset)   (w_post NULL:
+ *                                                   b stays)
+ *     x'  = residual_scale * x + branch_scale * act(gate) * b  -> x_out
+ *     xn  = x' * rsqrt(mean(x'^2) + eps) * (w_pre + w_offset)  -> xn, and in
+ *           8 bits -> xq, xq_scale
+ *   y NULL: no block behind the row: x' = x, nothing of the first three lines
+ *   is done (y2 and gate must be NULL), the plain norm before the first block.
+ *   x' is rounded to x's type before it is normed, so that xn is the norm of
+ *   what x_out holds.  All arithmetic is f32 (a row whose sum of squares
+ *   leaves the f32 range is summed again at another scale); one rounding per
+ *   output.  NaN and infinities of a row stay in that row.
+ *   x:       [T][H] in x_dtype, rows ldx elements apart (0 = H).
+ *   y, y2:   [T][H] in y_dtype, rows ldy elements apart (0 = H).
+ *   y2_gate: f32 [T], logits of the second branch's gate, or NULL.
+ *   gate:    f32, [T] (HFQ_GATE_TOKEN), [H] (HFQ_GATE_CHANNEL) or contiguous
+ *            [T][H] (HFQ_GATE_FULL); NULL with HFQ_GATE_NONE.  gate_act:
+ *            HFQ_GATE_LINEAR (as it is) or HFQ_GATE_SIGMOID.
+ *   x_out:   [T][H] in x_dtype, rows ldx apart, or NULL; it may be x itself
+ *            (x_out == x), else it must not overlap an input.
+ *   xn:      contiguous [T][H] in xn_dtype, or NULL.  w_pre NULL with xn or
+ *            xq: the bare norm (a weight of 1).
+ *   xq, xq_scale: int8 [T][round16(H)] (round16: up to a multiple of 16; the
+ *            tail of a row is written as 0) and f32 [T], both or neither: the
+ *            bits that q8_quantize_rows gives for the xn of xn_dtype.  xn may
+ *            be NULL then.
+ *   w_post, w_pre: [H] in w_dtype.
+ *   At least one of x_out, xn and xq is wanted.  1 <= H <= 8192,
+ *   1 <= T <= 65536, eps >= 0, every scale finite, pointers aligned to their
+ *   type.  Rows whose addresses are all 16-byte aligned, with H a multiple of
+ *   8, are read 16 bytes at a time.
+ */
+#define HFQ_GATE_NONE 0
+#define HFQ_GATE_TOKEN 1
+#define HFQ_GATE_CHANNEL 2
+#define HFQ_GATE_FULL 3
+#define HFQ_GATE_LINEAR 0
+#define HFQ_GATE_SIGMOID 1
+typedef struct {
+    const void *w_post;
+    const void *w_pre;
+    hfq_dtype w_dtype;
+    float eps;
+    float w_offset;
+    float residual_scale;
+    float branch_scale;
+    int gate_kind;
+    int gate_act;
+} moe_norm_rule;
+hfq_status moe_norm_residual(const moe_norm_rule *rule, int T, int H, const void *x, hfq_dtype x_dtype,
+                             int ldx, const void *y, const void *y2, hfq_dtype y_dtype, int ldy,
+                             const float *y2_gate, const float *gate, void *x_out, void *xn,
+                             hfq_dtype xn_dtype, int8_t *xq, float *xq_scale, void *stream);
+
+/*
+ * Dense products in 8-bit integers, for what stands beside the routed experts
+ * (a shared expert, a projection): one scale per token, one per output channel.
+ *
+ * q8_quantize_rows: q[r][c] = rint(v * 127 / amax_r) (half to even) and
+ * scale[r] = amax_r / 127 with amax_r = max_c |v[r][c]|; q is the nearest
+ * integer to the exact quotient.  A row of zeros gives scale 0 and q 0; a row
+ * that holds an infinity or a NaN gives scale NaN and q 0, so that every
+ * product with it is NaN.
+ *   act HFQ_ACT_NONE: v = x, [rows][cols] in x_dtype, rows ldx elements apart
+ *           (0 = cols).
+ *   act HFQ_ACT_SWIGLU: x is [rows][2 cols], gate first: v = silu(x[c]) *
+ *           x[cols + c] in f32 (0 = 2 cols apart): the hidden row of a shared
+ *           expert, ready for its down product.
+ *   q:      int8, rows ldq bytes apart (0 = round16(cols), cols rounded up to
+ *           a multiple of 16; else a multiple of 16, >= cols), 16-byte
+ *           aligned; the tail [cols, round16(cols)) of a row is written as 0.
+ *   scale:  f32 [rows].
+ *   Weights [N][K] are quantised by the same call: a row is a channel.
+ *
+ * q8_matmul: y[t][n] = (sum_k xq[t][k] * wq[n][k]) * xs[t] * ws[n], the sum
+ * exact in 32-bit integers, the rest f32 with one rounding to y's type.
+ *   xq, wq: int8 [T][K], [N][K], rows ldxq, ldw bytes apart (0 = round16(K);
+ *           else a multiple of 16, >= K), 16-byte aligned; bytes behind K are
+ *           not used.  Any value of -128 .. 127 may stand in them.
+ *   y:      [T][N] in y_dtype, rows ldy elements apart (0 = N; else >= N).
+ *
+ * q8_linear: y = q8_matmul(q8_quantize_rows(x), wq): the same bits as the two
+ * calls, in one launch where the tokens are few.
+ *   workspace: q8_linear_workspace_bytes(T, K, N) bytes of device scratch
+ *           (may be NULL when that is 0), 256-byte aligned, with no state kept
+ *           between calls; calls that share one must be ordered.
+ *   Limits: 1 <= T, rows <= 65536, 1 <= K, cols <= 16384, 1 <= N <= 65536;
+ *           x and y aligned to their type.
+ */
+#define HFQ_ACT_NONE 0
+#define HFQ_ACT_SWIGLU 1
+#define HFQ_Q8_MAX_K 16384
+hfq_status q8_quantize_rows(const void *x, hfq_dtype x_dtype, int ldx, int rows, int cols, int act,
+                            int8_t *q, int ldq, float *scale, void *stream);
+hfq_status q8_matmul(const int8_t *xq, int ldxq, const float *xs, int T, int K, const int8_t *wq, int ldw,
+                     const float *ws, int N, void *y, hfq_dtype y_dtype, int ldy, void *stream);
+size_t q8_linear_workspace_bytes(int T, int K, int N);
+hfq_status q8_linear(const void *x, hfq_dtype x_dtype, int ldx, int T, int K, const int8_t *wq, int ldw,
+                     const float *ws, int N, void *y, hfq_dtype y_dtype, int ldy, void *workspace,
+                     size_t ws_bytes, void *stream);
+
+/*
  * One MoE layer's experts [TABLE][PCIE].
  *   expert_ptr: DEVICE array [n_experts] of base addresses of the packed
  *               experts, each 16-byte aligned; an address may be HBM or a
