@@ -159,33 +159,33 @@ def _nbytes(a) -> int:
     return int(a.numel() * a.element_size())
 
 
-_I32, _I8 = 16, 17                       # operand types besides HFQ_F32 and HFQ_BF16
+_I32, _I8, _ANY = 16, 17, 18               # operand types besides HFQ_F32 and HFQ_BF16
 _types = {}
 
 
 def _operands(*ops) -> None:
     """Checks the operands (name, tensor, type, elements): a CUDA tensor of the
-    current device (whose stream the call goes to), of that type (None: any),
-    its last dimension dense, with at least that many elements behind its
-    address; or a raw device address, which is the caller's word."""
+    current device (whose stream the call goes to), of that type, its last
+    dimension dense, with at least that many elements behind its address; or a
+    raw device address, which is the caller's word."""
     torch = sys.modules.get("torch")
-    if torch is not None and not _types:
-        _types.update({HFQ_F32: (torch.float32,), HFQ_BF16: (torch.bfloat16, torch.int16, torch.uint16),
-                       _I32: (torch.int32,), _I8: (torch.int8,)})
-    device = None
+    if torch is None or not torch.cuda.is_initialized():
+        device = None
+    else:
+        device = torch._C._cuda_getDevice()
+        if not _types:
+            _types.update({HFQ_F32: (torch.float32,), HFQ_BF16: (torch.bfloat16, torch.int16, torch.uint16),
+                           _I32: (torch.int32,), _I8: (torch.int8,),
+                           _ANY: (torch.uint8, torch.int8, torch.int16, torch.int32, torch.int64, torch.float32)})
     for name, t, kind, n in ops:
-        if t is None or isinstance(t, int):
+        if t is None or type(t) is int:
             continue
-        if torch is None or not isinstance(t, torch.Tensor):
-            raise HfqError(-1, f"{name} is neither a CUDA tensor nor a device address")
-        if device is None:
-            device = torch.cuda.current_device() if torch.cuda.is_available() else None
-        if not t.is_cuda or t.get_device() != device:
-            raise HfqError(-1, f"{name} is on {t.device}, not on the current CUDA device")
-        if kind is None:
-            continue
+        if device is None or not isinstance(t, torch.Tensor) or t.get_device() != device:
+            raise HfqError(-1, f"{name} is neither a tensor of the current CUDA device nor a device address")
         if t.dtype not in _types.get(kind, ()):
             raise HfqError(-1, f"{name} is {t.dtype}, which is not the type the call names")
+        if t.is_contiguous() and t.numel() >= n:
+            continue
         if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
             raise HfqError(-1, f"{name}: the elements of a row are not next to each other")
         if t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < n:
@@ -195,7 +195,11 @@ def _operands(*ops) -> None:
 def _stream(s):
     if s is None:
         torch = sys.modules.get("torch")
-        if torch is not None and torch.cuda.is_available():
+        if torch is None:
+            return None
+        if torch.cuda.is_initialized():
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        if torch.cuda.is_available():
             return torch.cuda.current_stream().cuda_stream
         return None
     if isinstance(s, int):
@@ -269,7 +273,7 @@ def moe_route_scored(logits, logits_dtype: int, T: int, E: int, k: int, rule: Ro
     """Top-k routing by scores and a bias, with groups; lists as moe_route's."""
     _operands(("logits", logits, logits_dtype, (T - 1) * (ld or E) + E), ("bias", bias, HFQ_F32, E),
               ("idx", idx, _I32, T * k), ("wts", wts, HFQ_F32, T * k), ("cnt", cnt, _I32, E),
-              ("off", off, _I32, E + 1), ("perm", perm, _I32, T * k), ("workspace", workspace, None, 0))
+              ("off", off, _I32, E + 1), ("perm", perm, _I32, T * k), ("workspace", workspace, _ANY, 0))
     ws_bytes = _nbytes(workspace) if workspace is not None else 0
     _check(lib().moe_route_scored(_ptr(logits), logits_dtype, ld, T, E, _ptr(bias),
                                   ctypes.byref(rule.struct), k, _ptr(idx), _ptr(wts), _ptr(cnt),
@@ -341,7 +345,7 @@ def q8_linear(x, x_dtype: int, T: int, K: int, wq, ws, N: int, y, y_dtype: int, 
     k16 = -(-K // 16) * 16
     _operands(("x", x, x_dtype, (T - 1) * (ldx or K) + K), ("wq", wq, _I8, (N - 1) * (ldw or k16) + k16),
               ("ws", ws, HFQ_F32, N), ("y", y, y_dtype, (T - 1) * (ldy or N) + N),
-              ("workspace", workspace, None, 0))
+              ("workspace", workspace, _ANY, 0))
     ws_bytes = _nbytes(workspace) if workspace is not None else 0
     _check(lib().q8_linear(_ptr(x), x_dtype, ldx, T, K, _ptr(wq), ldw, _ptr(ws), N, _ptr(y), y_dtype, ldy,
                            _ptr(workspace), ws_bytes, _stream(stream)))
