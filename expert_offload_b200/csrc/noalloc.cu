@@ -12,6 +12,7 @@
 #include <mutex>
 
 #include "device.cuh"
+#include "q8.cuh"
 
 namespace hfq {
 namespace {
@@ -65,6 +66,8 @@ hfq_status noalloc_status(cudaStream_t s)
         std::lock_guard<std::mutex> g(g_mu);
         if (dev >= 0 && dev < kMaxDevices) scratch = g_scratch_ptr[dev];
     }
+    const hfq_status q8 = q8_status(s);
+    if (q8) return q8;
     if (!scratch) return ok();
     unsigned word = 0;
     e = cudaMemcpyAsync(&word, scratch, sizeof word, cudaMemcpyDeviceToHost, s);

@@ -7,7 +7,7 @@
 // Bound by memory: at bf16 streams and an f32 block output 20 bytes an element.
 #include <cfloat>
 
-#include "quant8.cuh"
+#include "rows.cuh"
 
 namespace hfq {
 namespace {
@@ -26,43 +26,6 @@ struct Args {
 };
 
 __device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
-
-// Eight elements of a row as they lie in memory (plain loads: x may be
-// rewritten in place).
-struct Raw8 {
-    uint4 a, b;
-};
-
-template <bool BF16>
-__device__ __forceinline__ Raw8 load_raw8(const void *p, size_t i)
-{
-    Raw8 r;
-    if (BF16) {
-        r.a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
-        r.b = r.a;
-    } else {
-        r.a = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i)[0];
-        r.b = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i)[1];
-    }
-    return r;
-}
-
-template <bool BF16>
-__device__ __forceinline__ void expand8(const Raw8 &r, float (&v)[8])
-{
-    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = BF16 ? __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) : __uint_as_float(w[i]);
-}
-
-__device__ __forceinline__ uint32_t two_bf16(float lo, float hi)
-{
-    return (uint32_t)float_to_bf16_bits(lo) | (uint32_t)float_to_bf16_bits(hi) << 16;
-}
-
-// Rounds v to bf16 (as a float).
-__device__ __forceinline__ float round_bf16(float v) { return bf16_bits_to_float(float_to_bf16_bits(v)); }
 
 // The elements of thread `tid` of a row: with VEC chunks of 8 neighbours, 8
 // elements apart from the next thread's; else single elements, a block apart.
@@ -179,7 +142,7 @@ __device__ __forceinline__ float2 inv_rms(const float (&v)[NV][8], int H, float 
 }
 
 template <bool VEC, int NV, bool XB, bool YB>
-__global__ void __launch_bounds__(1024) norm_kernel(const Args a)
+__global__ void __launch_bounds__(NV * 256) norm_kernel(const Args a)
 {
     __shared__ float red[32];
     const int nt = blockDim.x;

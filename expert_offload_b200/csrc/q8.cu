@@ -2,7 +2,9 @@
 // output channel: q8_quantize_rows, q8_matmul, q8_linear.
 #include <algorithm>
 
-#include "quant8.cuh"
+#include "ptx.cuh"
+#include "q8.cuh"
+#include "rows.cuh"
 
 namespace hfq {
 namespace {
@@ -13,70 +15,178 @@ struct QuantArgs {
     int8_t *q;
     float *scale;
     size_t ldx, ldq;
-    int rows, cols, bf16, swiglu;
+    int rows, cols, bf16, swiglu, vec;
+    int per_row;                 // threads of a row, a power of two of at least 32
+    int early;                   // the next kernel may start before this one ends
 };
 
-__device__ __forceinline__ float load_value(const QuantArgs &a, size_t row, int c)
+// A row is read once: `per_row` threads hold it in registers, two chunks of 8
+// each, between the maximum and the bytes.  Bound by memory (3 bytes an
+// element of a bf16 row).
+__global__ void __launch_bounds__(1024) quantize_kernel(const QuantArgs a)
 {
-    const float g = load_act(a.x, a.bf16 ? HFQ_BF16 : HFQ_F32, row + c);
-    if (!a.swiglu) return g;
-    const float u = load_act(a.x, a.bf16 ? HFQ_BF16 : HFQ_F32, row + a.cols + c);
-    return g / (1.0f + expf(-g)) * u;
-}
-
-// One block a row: its largest magnitude, then its bytes.
-__global__ void __launch_bounds__(256) quantize_kernel(const QuantArgs a)
-{
-    __shared__ uint32_t red[8];
-    const int lane = threadIdx.x & 31;
-    const size_t r = blockIdx.x, row = r * a.ldx;
+    __shared__ uint32_t red[32];
+    if (a.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int j = threadIdx.x & (a.per_row - 1);
+    const size_t r = (size_t)blockIdx.x * (blockDim.x / a.per_row) + threadIdx.x / a.per_row;
+    const bool in = r < (size_t)a.rows;
+    float v[2][8];
     uint32_t top = 0;
-    for (int c = threadIdx.x; c < a.cols; c += 256) top = max(top, abs_bits(load_value(a, row, c)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = (i * a.per_row + j) * 8;
+        if (!in || c >= a.cols) continue;
+        const void *row = row_at(a.x, a.bf16, r * a.ldx);
+        load8(row, a.bf16, a.vec, c, a.cols, v[i]);
+        if (a.swiglu) {
+            float u[8];
+            load8(row_at(row, a.bf16, a.cols), a.bf16, a.vec, c, a.cols, u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] / (1.0f + expf(-v[i][e])) * u[e];
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = max(top, abs_bits(v[i][e]));
+    }
     top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) red[threadIdx.x >> 5] = top;
-    __syncthreads();
-    top = __reduce_max_sync(0xffffffffu, red[lane & 7]);
+    if (a.per_row > 32) {
+        if (lane == 0) red[warp] = top;
+        __syncthreads();
+        const int n = a.per_row / 32, w0 = warp & ~(n - 1);
+        top = __reduce_max_sync(0xffffffffu, red[w0 + (lane & (n - 1))]);
+    }
+    if (!in) return;
     const RowQuant q(top);
     int8_t *out = a.q + r * a.ldq;
-    for (int c = threadIdx.x; c < (int)round16(a.cols); c += 256)
-        out[c] = c < a.cols ? (int8_t)q(load_value(a, row, c)) : (int8_t)0;
-    if (threadIdx.x == 0) a.scale[r] = row_scale(top);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int c = (i * a.per_row + j) * 8;
+        if (c < a.cols)
+            *reinterpret_cast<uint2 *>(out + c) =
+                make_uint2(pack4(q(v[i][0]), q(v[i][1]), q(v[i][2]), q(v[i][3])),
+                           pack4(q(v[i][4]), q(v[i][5]), q(v[i][6]), q(v[i][7])));
+        else if (c < (int)round16(a.cols)) *reinterpret_cast<uint2 *>(out + c) = make_uint2(0u, 0u);
+    }
+    if (j == 0) a.scale[r] = row_scale(top);
 }
 
-// -------------------------------------------------------------- the product
-struct MatArgs {
-    const int8_t *xq, *wq;
-    const float *xs, *ws;
-    void *y;
-    size_t ldxq, ldw, ldy;
-    int T, K, N, y_bf16;
+// -------------------------------------------------- few tokens: dot products
+// Up to eight tokens read every weight once and do little with it, so the
+// product is bound by the weights' bytes; CUDA cores (dp4a) keep up, and one
+// launch does it all: while a warp's first weights are on their way, its block
+// quantises the tokens into shared memory.
+constexpr int kDotWarps = 8;
+constexpr int kAhead = 4;        // 16-byte loads in flight per channel and lane
+
+struct DotArgs {
+    Q8Mat m;                     // xq, xs: null where x is quantised here
+    const void *x;
+    size_t ldx;
+    int x_bf16, x_vec;
 };
 
-// One warp an output channel, eight tokens at a time.
-__global__ void __launch_bounds__(256) dot_kernel(const MatArgs a)
+template <int TT, int R>
+__global__ void __launch_bounds__(kDotWarps * 32) dot_kernel(const DotArgs a)
 {
-    const int n = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (n >= a.N) return;
-    for (int t0 = blockIdx.y * 8; t0 < a.T; t0 += gridDim.y * 8) {
-        int acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        for (int k = lane * 4; k < a.K; k += 128) {
-            const uint32_t keep = a.K - k >= 4 ? 0xffffffffu : (1u << 8 * (a.K - k)) - 1u;
-            const uint32_t w = *reinterpret_cast<const uint32_t *>(a.wq + (size_t)n * a.ldw + k) & keep;
+    extern __shared__ __align__(16) int8_t xs8[];          // [TT][kp], zeros behind K
+    __shared__ uint32_t top[TT];
+    const Q8Mat &m = a.m;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int n0 = (blockIdx.x * kDotWarps + warp) * R;
+    const int k16 = (int)round16(m.K), kp = (m.K + 511) / 512 * 512;
+    auto load = [&](int r, int k) {
+        return n0 + r < m.N && k < k16 ? ld_nc_v4(m.wq + (size_t)(n0 + r) * m.ldw + k) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    uint4 w[R][kAhead];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (t0 + i < a.T)
-                    acc[i] = __dp4a((int)w, *reinterpret_cast<const int *>(a.xq + (size_t)(t0 + i) * a.ldxq + k), acc[i]);
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+        for (int r = 0; r < R; ++r) w[r][u] = load(r, (u * 32 + lane) * 16);
+
+    const int groups = kp / 8;
+    if (a.x) {
+        if (tid < TT) top[tid] = 0;
+        __syncthreads();
+        for (int t = 0; t < m.T; ++t) {
+            const void *row = row_at(a.x, a.x_bf16, (size_t)t * a.ldx);
+            uint32_t big = 0;
+            for (int g = tid; g * 8 < m.K; g += kDotWarps * 32) {
+                float v[8];
+                load8(row, a.x_bf16, a.x_vec, g * 8, m.K, v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) big = max(big, abs_bits(v[e]));
+            }
+            big = __reduce_max_sync(0xffffffffu, big);
+            if (lane == 0) atomicMax(&top[t], big);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int sum = __reduce_add_sync(0xffffffffu, acc[i]);
-            if (lane == 0 && t0 + i < a.T) {
-                const float v = (float)sum * a.xs[t0 + i] * a.ws[n];
-                const size_t at = (size_t)(t0 + i) * a.ldy + n;
-                if (a.y_bf16) static_cast<uint16_t *>(a.y)[at] = float_to_bf16_bits(v);
-                else static_cast<float *>(a.y)[at] = v;
+        __syncthreads();
+        for (int t = 0; t < TT; ++t) {
+            const void *row = row_at(a.x, a.x_bf16, (size_t)t * a.ldx);
+            const RowQuant q(t < m.T ? top[t] : 0u);
+            for (int g = tid; g < groups; g += kDotWarps * 32) {
+                float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                if (t < m.T) load8(row, a.x_bf16, a.x_vec, g * 8, m.K, v);
+                *reinterpret_cast<uint2 *>(xs8 + t * kp + g * 8) =
+                    make_uint2(pack4(q(v[0]), q(v[1]), q(v[2]), q(v[3])), pack4(q(v[4]), q(v[5]), q(v[6]), q(v[7])));
             }
         }
+    } else {
+        for (int i = tid; i < TT * kp / 4; i += kDotWarps * 32) {
+            const int t = i / (kp / 4), k = (i - t * (kp / 4)) * 4;
+            uint32_t v = 0;
+            if (t < m.T && k < m.K) {
+                v = *reinterpret_cast<const uint32_t *>(m.xq + (size_t)t * m.ldxq + k);
+                if (m.K - k < 4) v &= (1u << 8 * (m.K - k)) - 1u;
+            }
+            *reinterpret_cast<uint32_t *>(xs8 + t * kp + k) = v;
+        }
+    }
+    __syncthreads();
+    if (n0 >= m.N) return;
+
+    int acc[R][TT];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[r][t] = 0;
+    for (int k0 = 0; k0 < kp; k0 += kAhead * 512) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int k = k0 + (u * 32 + lane) * 16;
+            if (k0 + u * 512 >= kp) break;
+            uint4 c[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                c[r] = w[r][u];
+                w[r][u] = load(r, k + kAhead * 512);
+            }
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(xs8 + t * kp + k);
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    acc[r][t] = __dp4a((int)c[r].x, (int)x.x, acc[r][t]);
+                    acc[r][t] = __dp4a((int)c[r].y, (int)x.y, acc[r][t]);
+                    acc[r][t] = __dp4a((int)c[r].z, (int)x.z, acc[r][t]);
+                    acc[r][t] = __dp4a((int)c[r].w, (int)x.w, acc[r][t]);
+                }
+            }
+        }
+    }
+    int mine = 0;                                          // lane t * R + r keeps the sum of (r, t)
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int sum = __reduce_add_sync(0xffffffffu, acc[r][t]);
+            if (lane == t * R + r) mine = sum;
+        }
+    const int t = lane / R, n = n0 + lane % R;
+    if (t < m.T && n < m.N) {
+        const float v = q8_value(mine, a.x ? row_scale(top[t]) : m.xs[t], m.ws[n]);
+        const size_t at = (size_t)t * m.ldy + n;
+        if (m.y_bf16) static_cast<uint16_t *>(m.y)[at] = float_to_bf16_bits(v);
+        else static_cast<float *>(m.y)[at] = v;
     }
 }
 
@@ -116,16 +226,44 @@ hfq_status check_out(const char *who, int T, int K, const int8_t *wq, int ldw, c
 }
 
 void launch_quantize(const void *x, bool bf16, size_t ldx, int rows, int cols, bool swiglu, int8_t *q, size_t ldq,
-                     float *scale, cudaStream_t s)
+                     float *scale, bool early, cudaStream_t s)
 {
-    const QuantArgs a{x, q, scale, ldx, ldq, rows, cols, bf16, swiglu};
-    quantize_kernel<<<rows, 256, 0, s>>>(a);
+    QuantArgs a{x, q, scale, ldx, ldq, rows, cols, bf16, swiglu, 0, 32, early};
+    const size_t size = bf16 ? 2 : 4;
+    a.vec = aligned16(x) && ldx * size % 16 == 0 && (!swiglu || cols * size % 16 == 0);
+    while (a.per_row * 16 < cols) a.per_row *= 2;
+    const int block = std::max(a.per_row, 256), per = block / a.per_row;
+    quantize_kernel<<<(rows + per - 1) / per, block, 0, s>>>(a);
 }
 
-void launch_matmul(const MatArgs &a, cudaStream_t s)
+template <int TT, int R>
+cudaError_t launch_dot(const DotArgs &a, int smem, cudaStream_t s)
 {
-    const dim3 grid((a.N + 7) / 8, std::min((a.T + 7) / 8, 1024));
-    dot_kernel<<<grid, 256, 0, s>>>(a);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(dot_kernel<TT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    const int per = kDotWarps * R;
+    dot_kernel<TT, R><<<(a.m.N + per - 1) / per, kDotWarps * 32, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+// Tokens that the dot kernel takes.
+constexpr int kDotTokens = 8;
+bool takes_dot(int T) { return T <= kDotTokens; }
+
+hfq_status run_dot(const DotArgs &a, cudaStream_t s)
+{
+    const int kp = (a.m.K + 511) / 512 * 512;
+    const bool wide = a.m.N > 2 * kDotWarps * 148;         // channels for two a warp on every SM
+    const int T = a.m.T;
+    cudaError_t e;
+    if (T == 1) e = wide ? launch_dot<1, 2>(a, kp, s) : launch_dot<1, 1>(a, kp, s);
+    else if (T == 2) e = wide ? launch_dot<2, 2>(a, 2 * kp, s) : launch_dot<2, 1>(a, 2 * kp, s);
+    else if (T <= 4) e = wide ? launch_dot<4, 2>(a, 4 * kp, s) : launch_dot<4, 1>(a, 4 * kp, s);
+    else e = wide ? launch_dot<8, 2>(a, 8 * kp, s) : launch_dot<8, 1>(a, 8 * kp, s);
+    if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "8-bit product launch: %s", cudaGetErrorString(e));
+    return HFQ_OK;
 }
 
 }  // namespace
@@ -146,7 +284,7 @@ hfq_status q8_quantize_rows(const void *x, hfq_dtype x_dtype, int ldx, int rows,
     if ((st = check_q("q8_quantize_rows", "q", q, ldq, cols))) return st;
     if (misaligned(scale, HFQ_F32)) return fail(HFQ_ERR_ALIGN, "q8_quantize_rows: scale must be 4-byte aligned");
     launch_quantize(x, x_dtype == HFQ_BF16, ldx ? ldx : width, rows, cols, act == HFQ_ACT_SWIGLU, q,
-                    ldq ? ldq : round16(cols), scale, (cudaStream_t)stream);
+                    ldq ? ldq : round16(cols), scale, false, (cudaStream_t)stream);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return fail(HFQ_ERR_CUDA, "q8_quantize_rows launch: %s", cudaGetErrorString(err));
     return ok();
@@ -160,17 +298,16 @@ hfq_status q8_matmul(const int8_t *xq, int ldxq, const float *xs, int T, int K, 
     if (st) return st;
     if ((st = check_q("q8_matmul", "xq", xq, ldxq, K))) return st;
     if (misaligned(xs, HFQ_F32)) return fail(HFQ_ERR_ALIGN, "q8_matmul: xs must be 4-byte aligned");
-    const MatArgs a{xq, wq, xs, ws, y, ldxq ? (size_t)ldxq : round16(K), ldw ? (size_t)ldw : round16(K),
-                    (size_t)(ldy ? ldy : N), T, K, N, y_dtype == HFQ_BF16};
-    launch_matmul(a, (cudaStream_t)stream);
-    const cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return fail(HFQ_ERR_CUDA, "q8_matmul launch: %s", cudaGetErrorString(err));
-    return ok();
+    const Q8Mat m{xq, wq, xs, ws, y, ldxq ? (size_t)ldxq : round16(K), ldw ? (size_t)ldw : round16(K),
+                  (size_t)(ldy ? ldy : N), T, K, N, y_dtype == HFQ_BF16};
+    st = takes_dot(T) ? run_dot(DotArgs{m, nullptr, 0, 0, 0}, (cudaStream_t)stream)
+                      : launch_q8_tc(m, false, (cudaStream_t)stream);
+    return st ? st : ok();
 }
 
 size_t q8_linear_workspace_bytes(int T, int K, int N)
 {
-    if (T < 1 || K < 1 || N < 1) return 0;
+    if (T < 1 || K < 1 || N < 1 || takes_dot(T)) return 0;
     return ((size_t)T * round16(K) + 255) / 256 * 256 + (size_t)T * sizeof(float);
 }
 
@@ -187,16 +324,24 @@ hfq_status q8_linear(const void *x, hfq_dtype x_dtype, int ldx, int T, int K, co
         return fail(HFQ_ERR_WORKSPACE, "q8_linear: needs %zu bytes of workspace", need);
     if (need && ((uintptr_t)workspace & 255))
         return fail(HFQ_ERR_ALIGN, "q8_linear: the workspace must be 256-byte aligned");
-    int8_t *xq = static_cast<int8_t *>(workspace);
-    float *xs = reinterpret_cast<float *>(xq + ((size_t)T * round16(K) + 255) / 256 * 256);
+    const bool bf16 = x_dtype == HFQ_BF16;
+    const size_t ld = ldx ? ldx : K;
     cudaStream_t s = (cudaStream_t)stream;
-    launch_quantize(x, x_dtype == HFQ_BF16, ldx ? ldx : K, T, K, false, xq, round16(K), xs, s);
-    const MatArgs a{xq, wq, xs, ws, y, round16(K), ldw ? (size_t)ldw : round16(K), (size_t)(ldy ? ldy : N), T, K, N,
-                    y_dtype == HFQ_BF16};
-    launch_matmul(a, s);
-    const cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return fail(HFQ_ERR_CUDA, "q8_linear launch: %s", cudaGetErrorString(err));
-    return ok();
+    Q8Mat m{nullptr, wq, nullptr, ws, y, round16(K), ldw ? (size_t)ldw : round16(K), (size_t)(ldy ? ldy : N), T, K, N,
+            y_dtype == HFQ_BF16};
+    if (takes_dot(T)) {
+        st = run_dot(DotArgs{m, x, ld, bf16, aligned16(x) && ld * (bf16 ? 2 : 4) % 16 == 0}, s);
+    } else {
+        int8_t *xq = static_cast<int8_t *>(workspace);
+        float *xs = reinterpret_cast<float *>(xq + ((size_t)T * round16(K) + 255) / 256 * 256);
+        launch_quantize(x, bf16, ld, T, K, false, xq, round16(K), xs, true, s);
+        const cudaError_t err = cudaGetLastError();
+        if (err != cudaSuccess) return fail(HFQ_ERR_CUDA, "q8_linear launch: %s", cudaGetErrorString(err));
+        m.xq = xq;
+        m.xs = xs;
+        st = launch_q8_tc(m, true, s);
+    }
+    return st ? st : ok();
 }
 
 }  // extern "C"

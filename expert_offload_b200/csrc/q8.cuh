@@ -1,0 +1,27 @@
+// q8.cuh - what the 8-bit product's translation units share.
+#pragma once
+
+#include "quant8.cuh"
+
+namespace hfq {
+
+// One product y = (xq wq^T) * xs * ws.
+struct Q8Mat {
+    const int8_t *xq, *wq;
+    const float *xs, *ws;
+    void *y;
+    size_t ldxq, ldw, ldy;       // bytes, bytes, elements
+    int T, K, N, y_bf16;
+};
+
+// The value of an output from its integer sum: one order of the two products
+// everywhere, so that every path gives the same bits.
+__device__ __forceinline__ float q8_value(int acc, float xs, float ws) { return (float)acc * xs * ws; }
+
+// Tensor-core product (q8_tc.cu).  `chained`: the kernel before it on the
+// stream is the quantiser of xq, which started after everything that wrote wq.
+hfq_status launch_q8_tc(const Q8Mat &a, bool chained, cudaStream_t s);
+// Status word of its bounded waits on the current device; clears it.
+hfq_status q8_status(cudaStream_t s);
+
+}  // namespace hfq

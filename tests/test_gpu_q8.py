@@ -248,3 +248,27 @@ def test_offsets_past_32_bits(eo):
     q, s = torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda()
     for a, b in ((0, 300), (T - 300, T)):
         _close(y[a:b], _exact(q[a:b], s[a:b], w, ws, K), "bf16")
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(eo):
+    """The test hook makes the tensor-core kernel wait for an arrival that never
+    comes; the wait is bounded, the status says so once."""
+    T, K, N = 40, 1024, 300
+    xq, xs = torch.ones(T, K, dtype=torch.int8, device="cuda"), torch.ones(T, device="cuda")
+    w, ws = _weights(1, N, K, K)
+    y = torch.empty(T, N, device="cuda")
+    eo.hfq_set_option(eo.OPT_WAIT_TIMEOUT_NS, 2_000_000)
+    try:
+        for split_k in (K, 128):                         # a cluster, and one CTA alone
+            eo.hfq_set_option(eo.OPT_TEST_MISSING_ARRIVALS, 1)
+            eo.q8_matmul(xq, xs, T, split_k, w, ws, N, y, eo.HFQ_F32, ldxq=K, ldw=K)
+            with pytest.raises(eo.HfqError) as e:
+                eo.hfq_workspace_status(None)
+            assert e.value.status == -6
+            eo.hfq_workspace_status(None)
+            eo.q8_matmul(xq, xs, T, split_k, w, ws, N, y, eo.HFQ_F32, ldxq=K, ldw=K)
+            eo.hfq_workspace_status(None)
+            _close(y, _exact(xq, xs, w, ws, split_k), "f32")
+    finally:
+        eo.hfq_set_option(eo.OPT_WAIT_TIMEOUT_NS, 1_000_000_000)
+        eo.hfq_set_option(eo.OPT_TEST_MISSING_ARRIVALS, 0)
