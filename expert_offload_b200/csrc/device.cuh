@@ -58,6 +58,13 @@ __device__ __forceinline__ uint16_t float_to_bf16_bits(float f)
     return __bfloat16_as_ushort(__float2bfloat16_rn(f));
 }
 
+// Two bf16, `lo` in the lower half, by one conversion.
+__device__ __forceinline__ uint32_t two_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
 
 // Loads activation element i of a row stored as f32 or bf16.

@@ -223,20 +223,19 @@ __global__ void __launch_bounds__(NV * 256) norm_kernel(const Args a)
                 if (row.in(c, i)) top = max(top, abs_bits(x[c][i]));
             }
         top = block_max(top, red, nt);
-        const RowQuant q(top);
+        const RowQuant<true> qb(top);
+        const RowQuant<false> qf(top);
         const size_t ldq = round16(a.H);
         int8_t *out = a.xq + (size_t)t * ldq;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
+            const uint2 w = a.xn_bf16 ? qb(x[c]) : qf(x[c]);
             if (VEC) {
-                if (row.in(c, 0))
-                    *reinterpret_cast<uint2 *>(out + row.at(c, 0)) =
-                        make_uint2(pack4(q(x[c][0]), q(x[c][1]), q(x[c][2]), q(x[c][3])),
-                                   pack4(q(x[c][4]), q(x[c][5]), q(x[c][6]), q(x[c][7])));
+                if (row.in(c, 0)) *reinterpret_cast<uint2 *>(out + row.at(c, 0)) = w;
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (row.in(c, i)) out[row.at(c, i)] = (int8_t)q(x[c][i]);
+                    if (row.in(c, i)) out[row.at(c, i)] = (int8_t)((i < 4 ? w.x : w.y) >> 8 * (i & 3));
             }
         }
         if (threadIdx.x < ldq - a.H) out[a.H + threadIdx.x] = 0;

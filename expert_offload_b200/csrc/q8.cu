@@ -20,10 +20,11 @@ struct QuantArgs {
     int early;                   // the next kernel may start before this one ends
 };
 
-// A row is read once: `per_row` threads hold it in registers, two chunks of 8
+// A row is read once: `per_row` threads hold it in registers, NV chunks of 8
 // each, between the maximum and the bytes.  Bound by memory (3 bytes an
 // element of a bf16 row).
-__global__ void __launch_bounds__(1024) quantize_kernel(const QuantArgs a)
+template <int NV, bool BF16>
+__global__ void __launch_bounds__(512) quantize_kernel(const QuantArgs a)
 {
     __shared__ uint32_t red[32];
     if (a.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -31,15 +32,15 @@ __global__ void __launch_bounds__(1024) quantize_kernel(const QuantArgs a)
     const int j = threadIdx.x & (a.per_row - 1);
     const size_t r = (size_t)blockIdx.x * (blockDim.x / a.per_row) + threadIdx.x / a.per_row;
     const bool in = r < (size_t)a.rows;
-    float v[2][8];
+    float v[NV][8];
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NV; ++i) {
         const int c = (i * a.per_row + j) * 8;
         if (!in || c >= a.cols) continue;
         const void *row = row_at(a.x, a.bf16, r * a.ldx);
-        load8(row, a.bf16, a.vec, c, a.cols, v[i]);
-        if (a.swiglu) {
+        load8(row, BF16 || a.bf16, a.vec, c, a.cols, v[i]);
+        if (!BF16 && a.swiglu) {
             float u[8];
             load8(row_at(row, a.bf16, a.cols), a.bf16, a.vec, c, a.cols, u);
 #pragma unroll
@@ -56,15 +57,13 @@ __global__ void __launch_bounds__(1024) quantize_kernel(const QuantArgs a)
         top = __reduce_max_sync(0xffffffffu, red[w0 + (lane & (n - 1))]);
     }
     if (!in) return;
-    const RowQuant q(top);
+    const RowQuant<BF16> q(top);                           // BF16: bf16 rows as they are
     int8_t *out = a.q + r * a.ldq;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NV; ++i) {
         const int c = (i * a.per_row + j) * 8;
         if (c < a.cols)
-            *reinterpret_cast<uint2 *>(out + c) =
-                make_uint2(pack4(q(v[i][0]), q(v[i][1]), q(v[i][2]), q(v[i][3])),
-                           pack4(q(v[i][4]), q(v[i][5]), q(v[i][6]), q(v[i][7])));
+            *reinterpret_cast<uint2 *>(out + c) = q(v[i]);
         else if (c < (int)round16(a.cols)) *reinterpret_cast<uint2 *>(out + c) = make_uint2(0u, 0u);
     }
     if (j == 0) a.scale[r] = row_scale(top);
@@ -122,12 +121,11 @@ __global__ void __launch_bounds__(kDotWarps * 32) dot_kernel(const DotArgs a)
         __syncthreads();
         for (int t = 0; t < TT; ++t) {
             const void *row = row_at(a.x, a.x_bf16, (size_t)t * a.ldx);
-            const RowQuant q(t < m.T ? top[t] : 0u);
+            const RowQuant<false> q(t < m.T ? top[t] : 0u);
             for (int g = tid; g < groups; g += kDotWarps * 32) {
                 float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                 if (t < m.T) load8(row, a.x_bf16, a.x_vec, g * 8, m.K, v);
-                *reinterpret_cast<uint2 *>(xs8 + t * kp + g * 8) =
-                    make_uint2(pack4(q(v[0]), q(v[1]), q(v[2]), q(v[3])), pack4(q(v[4]), q(v[5]), q(v[6]), q(v[7])));
+                *reinterpret_cast<uint2 *>(xs8 + t * kp + g * 8) = q(v);
             }
         }
     } else {
@@ -231,9 +229,14 @@ void launch_quantize(const void *x, bool bf16, size_t ldx, int rows, int cols, b
     QuantArgs a{x, q, scale, ldx, ldq, rows, cols, bf16, swiglu, 0, 32, early};
     const size_t size = bf16 ? 2 : 4;
     a.vec = aligned16(x) && ldx * size % 16 == 0 && (!swiglu || cols * size % 16 == 0);
-    while (a.per_row * 16 < cols) a.per_row *= 2;
-    const int block = std::max(a.per_row, 256), per = block / a.per_row;
-    quantize_kernel<<<(rows + per - 1) / per, block, 0, s>>>(a);
+    const int nv = cols <= 4096 ? 2 : 4;
+    while (a.per_row * 8 * nv < cols) a.per_row *= 2;      // at most 512
+    const int block = std::max(a.per_row, 256), per = block / a.per_row, grid = (rows + per - 1) / per;
+    const bool exact = bf16 && !swiglu;
+    if (nv == 2 && exact) quantize_kernel<2, true><<<grid, block, 0, s>>>(a);
+    else if (nv == 2) quantize_kernel<2, false><<<grid, block, 0, s>>>(a);
+    else if (exact) quantize_kernel<4, true><<<grid, block, 0, s>>>(a);
+    else quantize_kernel<4, false><<<grid, block, 0, s>>>(a);
 }
 
 template <int TT, int R>

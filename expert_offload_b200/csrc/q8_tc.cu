@@ -114,6 +114,55 @@ __device__ __forceinline__ void store_y(const Q8Mat &m, int t, int n, float v)
     else static_cast<float *>(m.y)[at] = v;
 }
 
+// Writes 32 columns of a warp: lane's channel n (ws its scale), tokens t0 ..
+// t0 + 31 (xs: their scales, shared memory).  All values first, then the
+// stores, those without a condition where the whole block lies inside: the
+// values of 32 columns are independent, a branch at each store would make them
+// wait for one another.  `pairs` (bf16 rows that allow 4-byte stores):
+// neighbours exchange halves, so that an even lane writes two channels of one
+// token and the odd lane the same two of the next.
+__device__ __forceinline__ void store_columns(const Q8Mat &m, int t0, int n, int lane, bool pairs, float ws,
+                                              const float *xs, const int (&v)[32])
+{
+    const bool inside = t0 + 32 <= m.T && n - lane + 32 <= m.N;      // the same in all lanes
+    if (pairs) {
+        uint32_t out[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            const float2 s = *reinterpret_cast<const float2 *>(xs + j);
+            const uint32_t w = two_bf16(q8_value(v[j], s.x, ws), q8_value(v[j + 1], s.y, ws));
+            const uint32_t o = __shfl_xor_sync(0xffffffffu, w, 1);
+            out[j / 2] = lane & 1 ? __byte_perm(o, w, 0x7632) : __byte_perm(w, o, 0x5410);
+        }
+        const int odd = lane & 1, nn = n & ~1;
+        uint16_t *p = static_cast<uint16_t *>(m.y) + (size_t)(t0 + odd) * m.ldy + nn;
+        if (inside) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j, p += 2 * m.ldy) *reinterpret_cast<uint32_t *>(p) = out[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j, p += 2 * m.ldy)
+                if (t0 + 2 * j + odd < m.T) {
+                    if (nn + 1 < m.N) *reinterpret_cast<uint32_t *>(p) = out[j];
+                    else if (nn < m.N) *p = (uint16_t)out[j];
+                }
+        }
+        return;
+    }
+    float f[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) f[j] = q8_value(v[j], xs[j], ws);
+    if (inside && !m.y_bf16) {
+        float *p = static_cast<float *>(m.y) + (size_t)t0 * m.ldy + n;
+#pragma unroll
+        for (int j = 0; j < 32; ++j, p += m.ldy) *p = f[j];
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (n < m.N && t0 + j < m.T) store_y(m, t0 + j, n, f[j]);
+    }
+}
+
 // ------------------------------------------------------------ one tile a CTA
 // Tiles of 128 channels x BT tokens; with split > 1 the CTAs of a cluster take
 // a share of K each and add their sums through distributed shared memory
@@ -123,8 +172,7 @@ template <int BT>
 struct TileCfg {
     static constexpr int kStages = 4;
     static constexpr int kA = kCh * kKb, kB = BT * kKb, kStage = kA + kB;
-    static constexpr int kPad = BT + 4;                              // ints of a channel's row in the exchange
-    static constexpr int kExch = kCh * kPad * 4;                     // bytes
+    static constexpr int kExch = kCh * BT * 4;                       // bytes of the exchange
     static constexpr int kSmem = 1024 + kStages * kStage;
     static constexpr int kSmemSplit = kSmem + kExch;
     static constexpr uint32_t kCols = BT < 32 ? 32 : BT;             // tensor-memory columns
@@ -138,6 +186,7 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
     extern __shared__ uint8_t raw[];
     uint8_t *buf = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t full[C::kStages], empty[C::kStages], done, never;
+    __shared__ __align__(16) float xs_of[4][32];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -221,20 +270,23 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
         if (ok) {
             if (a.split == 1) {
                 grid_dependency_wait();                    // xs comes from the kernel before, too
+                const bool pairs = m.y_bf16 && m.ldy % 2 == 0 && ((uintptr_t)m.y & 3) == 0;
                 const float ws = n < m.N ? m.ws[n] : 0.0f;
 #pragma unroll 1
                 for (int col = 0; col < tv; col += 32) {
                     int v[32];
                     tmem_ld32(trow + col, v);
-                    if (n < m.N)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (col + j < tv) store_y(m, t0 + col + j, n, q8_value(v[j], __ldg(m.xs + t0 + col + j), ws));
+                    __syncwarp();                            // the last columns' scales have been read
+                    xs_of[warp - 2][lane] = col + lane < tv ? __ldg(m.xs + t0 + col + lane) : 0.0f;
+                    __syncwarp();
+                    store_columns(m, t0 + col, n, lane, pairs, ws, xs_of[warp - 2], v);
                 }
             } else {
+                // four tokens of a channel are 16 bytes, next to those of the next
+                // channel: a warp's store is one run of 512 bytes for each owner
                 const int own = kCh / a.split, owner = ch / own;
                 const uint32_t mine = smem_u32(buf + C::kStages * C::kStage) +
-                                      (uint32_t)((rank * own + ch - owner * own) * C::kPad * 4);
+                                      (uint32_t)(rank * own * BT * 4 + (ch - owner * own) * 16);
                 const uint32_t dst = map_rank(mine, (uint32_t)owner);
 #pragma unroll 1
                 for (int col = 0; col < tv; col += 32) {
@@ -242,7 +294,8 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
                     tmem_ld32(trow + col, v);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4)
-                        if (col + j < tv) st_cluster_v4(dst + (uint32_t)(col + j) * 4, v[j], v[j + 1], v[j + 2], v[j + 3]);
+                        if (col + j < tv)
+                            st_cluster_v4(dst + (uint32_t)((col + j) / 4 * own * 16), v[j], v[j + 1], v[j + 2], v[j + 3]);
                 }
             }
         }
@@ -252,19 +305,221 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
         cluster_sync();
         grid_dependency_wait();
         const int own = kCh / a.split, tv = min(BT, m.T - t0);
-        const int *part = reinterpret_cast<const int *>(buf + C::kStages * C::kStage);
-        for (int i = threadIdx.x; i < own * tv; i += kThr) {
-            const int t = i / own, c = i - t * own, n = n0 + rank * own + c;
+        const int4 *part = reinterpret_cast<const int4 *>(buf + C::kStages * C::kStage);
+        for (int i = threadIdx.x; i < own * ((tv + 3) / 4); i += kThr) {
+            const int q = i / own, c = i - q * own, n = n0 + rank * own + c, t = t0 + 4 * q;
             if (n >= m.N) continue;
-            int sum = 0;
-            for (int r = 0; r < a.split; ++r) sum += part[(r * own + c) * C::kPad + t];
-            store_y(m, t0 + t, n, q8_value(sum, __ldg(m.xs + t0 + t), m.ws[n]));
+            int4 sum = make_int4(0, 0, 0, 0);
+            for (int r = 0; r < a.split; ++r) {
+                const int4 p = part[r * own * (BT / 4) + i];
+                sum.x += p.x, sum.y += p.y, sum.z += p.z, sum.w += p.w;
+            }
+            const float ws = __ldg(m.ws + n);
+            store_y(m, t, n, q8_value(sum.x, __ldg(m.xs + t), ws));
+            if (t + 1 < m.T) store_y(m, t + 1, n, q8_value(sum.y, __ldg(m.xs + t + 1), ws));
+            if (t + 2 < m.T) store_y(m, t + 2, n, q8_value(sum.z, __ldg(m.xs + t + 2), ws));
+            if (t + 3 < m.T) store_y(m, t + 3, n, q8_value(sum.w, __ldg(m.xs + t + 3), ws));
         }
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     if (warp == 1) tmem_dealloc(tmem, C::kCols);
+}
+
+// ------------------------------------------------ large products: CTA pairs
+// A pair of CTAs (cta_group::2) works on tiles of 256 channels x BT tokens: each
+// CTA brings its 128 channels and half of the tokens, the leader's MMAs read
+// both shared memories, and each CTA's tensor memory gets its own channels'
+// sums of all BT tokens.  A stage of 128 K bytes is thus 32 KB a CTA for 512
+// clocks of the tensor pipe (BT = 256), 64 bytes a clock, where a CTA alone
+// would need 96: more than L2 delivers to every SM.
+//
+// Persistent: a pair walks tiles with two accumulator buffers, so the
+// epilogue (8 warps) of a tile overlaps the MMAs of the next.
+constexpr int kEpiWarps = 8;
+constexpr int kPairThr = 64 + 32 * kEpiWarps;
+constexpr int kEpiParts = kEpiWarps / 4;  // of a tile's columns, each for four warps
+
+template <int BT>
+struct PairCfg {
+    static constexpr int kA = kCh * kKb, kB = BT / 2 * kKb, kStage = kA + kB;
+    static constexpr int kStages = 196608 / kStage;                  // 6 of 32 KB, 8 of 24 KB
+    static constexpr int kSmem = 1024 + kStages * kStage;
+    static constexpr uint32_t kCols = 2 * BT;
+};
+
+__device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrives on `bar` of both CTAs of the pair when all MMAs issued so far by
+// this thread are done.
+__device__ __forceinline__ void umma_commit_pair(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+// Tiled load into this CTA's shared memory that completes on a barrier of the
+// pair's leader (`bar`: its shared::cluster address).  No multicast.
+__device__ __forceinline__ void tma_load_2d_pair(void *dst, const void *map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+            "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// Tile `i` of the walk: bands of 8 channel tiles, in a band the channel tiles of
+// one token tile after the other's, so that the pairs at work share rows in L2.
+__device__ __forceinline__ void tile_of(int i, int ct, int tt, int &c, int &t)
+{
+    const int band = i / (8 * tt), c0 = band * 8, w = min(8, ct - c0), r = i - c0 * tt;
+    t = r / w;
+    c = c0 + r - t * w;
+}
+
+template <int BT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThr)
+q8_pair_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap)
+{
+    using C = PairCfg<BT>;
+    extern __shared__ uint8_t raw[];
+    uint8_t *buf = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+    __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], never;
+    __shared__ __align__(16) float xs_of[kEpiWarps][32];
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Q8Mat &m = a.m;
+    const int rank = (int)cluster_rank();
+    const int ct = (m.N + 2 * kCh - 1) / (2 * kCh), tt = (m.T + BT - 1) / BT;
+    const int nk = (m.K + kKb - 1) / kKb, tiles = ct * tt, first = (int)blockIdx.x / 2, step = (int)gridDim.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 2 * kEpiWarps);
+        }
+        mbar_init(&never, 1);
+        fence_mbar_init();
+        abort_flag = 0;
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_base)),
+                     "r"(C::kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after_sync();
+    const uint32_t tmem = tmem_base;
+    volatile int *abortp = &abort_flag;
+    grid_dependency_wait();
+
+    if (warp == 0 && lane == 0) {
+        int g = 0;                                       // stages filled so far
+        for (int i = first; i < tiles && !*abortp; i += step) {
+            int c, t;
+            tile_of(i, ct, tt, c, t);
+            const int n0 = c * 2 * kCh + rank * kCh, t0 = t * BT + rank * (BT / 2);
+            for (int k = 0; k < nk; ++k, ++g) {
+                const int s = g % C::kStages;
+                if (g >= C::kStages && !wait_bar(&empty[s], (uint32_t)(g / C::kStages - 1) & 1u, a.timeout_ns, abortp))
+                    break;
+                uint8_t *dst = buf + s * C::kStage;
+                const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+                if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * C::kStage);
+                tma_load_2d_pair(dst, &wmap, k * kKb, n0, bar);
+                tma_load_2d_pair(dst + C::kA, &xmap, k * kKb, t0, bar);
+            }
+        }
+        // the copies of this CTA have landed once the MMAs that read them are
+        // done; after an abort the waits that ran out gave them their time
+        for (int j = max(0, g - C::kStages); j < g; ++j)
+            wait_bar(&empty[j % C::kStages], (uint32_t)(j / C::kStages) & 1u, a.timeout_ns, abortp);
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        bool ok = !a.hook || wait_bar(&never, 0u, a.timeout_ns, abortp);
+        int g = 0, n = 0;
+        for (int i = first; ok && i < tiles; i += step, ++n) {
+            const int b = n & 1;
+            if (n >= 2 && !(ok = wait_bar(&tempty[b], (uint32_t)(n / 2 - 1) & 1u, a.timeout_ns, abortp))) break;
+            tc_fence_after_sync();
+            for (int k = 0; k < nk; ++k, ++g) {
+                const int s = g % C::kStages;
+                if (!(ok = wait_bar(&full[s], (uint32_t)(g / C::kStages) & 1u, a.timeout_ns, abortp))) break;
+                tc_fence_after_sync();
+                const uint64_t ad = umma_desc_sw128(buf + s * C::kStage);
+                const uint64_t bd = umma_desc_sw128(buf + s * C::kStage + C::kA);
+#pragma unroll
+                for (int j = 0; j < kKb / 32; ++j)
+                    umma_i8_pair(tmem + (uint32_t)(b * BT), ad + 2 * j, bd + 2 * j, idesc_i8(2 * kCh, BT), k > 0 || j > 0);
+                umma_commit_pair(&empty[s]);
+            }
+            umma_commit_pair(&tfull[b]);
+        }
+        // no MMA may run when the pair ends: its last commit has arrived
+        if (n > 0) wait_bar(&tfull[(n - 1) & 1], (uint32_t)((n - 1) / 2) & 1u, a.timeout_ns, nullptr);
+    } else if (warp >= 2) {
+        // the sums: warp w reads lanes 32 (w % 4) .. + 31, one part of the columns
+        constexpr int kPart = BT / kEpiParts;
+        const int part = (warp - 2) >> 2, ch = (warp & 3) * 32 + lane;
+        const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const bool pairs = m.y_bf16 && m.ldy % 2 == 0 && ((uintptr_t)m.y & 3) == 0;
+        int n = 0;
+        for (int i = first; i < tiles; i += step, ++n) {
+            int c, t;
+            tile_of(i, ct, tt, c, t);
+            const int b = n & 1, nn = c * 2 * kCh + rank * kCh + ch, t0 = t * BT;
+            const float ws = nn < m.N ? __ldg(m.ws + nn) : 0.0f;
+            if (!wait_bar(&tfull[b], (uint32_t)(n / 2) & 1u, a.timeout_ns, abortp)) break;
+            tc_fence_after_sync();
+#pragma unroll 1
+            for (int col = part * kPart; col < (part + 1) * kPart; col += 32) {
+                int v[32];
+                tmem_ld32(trow + (uint32_t)(b * BT + col), v);
+                if (col + 32 == (part + 1) * kPart) {     // this warp's last read of the buffer
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(map_rank(smem_u32(&tempty[b]), 0));
+                }
+                const int tc = t0 + col;
+                if (tc >= m.T) continue;
+                __syncwarp();                                // the last columns' scales have been read
+                xs_of[warp - 2][lane] = tc + lane < m.T ? __ldg(m.xs + tc + lane) : 0.0f;
+                __syncwarp();
+                store_columns(m, tc, nn, lane, pairs, ws, xs_of[warp - 2], v);
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();                                      // the other CTA may still arrive on barriers here
+    tc_fence_after_sync();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
 }
 
 // ------------------------------------------------------------- the host side
@@ -318,6 +573,26 @@ cudaError_t launch_tile(Args a, const CUtensorMap &wmap, const CUtensorMap &xmap
     return cudaLaunchKernelEx(&cfg, q8_tile_kernel<BT>, a, wmap, xmap);
 }
 
+template <int BT>
+cudaError_t launch_pair(const Args &a, const CUtensorMap &wmap, const CUtensorMap &xmap, cudaStream_t s)
+{
+    using C = PairCfg<BT>;
+    cudaError_t e = cudaFuncSetAttribute(q8_pair_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    const int tiles = (a.m.N + 2 * kCh - 1) / (2 * kCh) * ((a.m.T + BT - 1) / BT);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * std::min(tiles, sm_count() / 2));
+    cfg.blockDim = dim3(kPairThr);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.chained ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, q8_pair_kernel<BT>, a, wmap, xmap);
+}
+
 }  // namespace
 
 hfq_status launch_q8_tc(const Q8Mat &m, bool chained, cudaStream_t s)
@@ -328,14 +603,24 @@ hfq_status launch_q8_tc(const Q8Mat &m, bool chained, cudaStream_t s)
     a.timeout_ns = option_wait_timeout_ns();
     a.chained = chained;
     a.hook = option_take_extra_arrivals();
-    const int bt = m.T <= 16 ? 16 : m.T <= 32 ? 32 : m.T <= 64 ? 64 : 128;
+    CUtensorMap wmap, xmap;
+    if (!encode(&wmap, m.wq, m.K, m.N, m.ldw, kCh))
+        return fail(HFQ_ERR_CUDA, "8-bit product: tensor map encoding failed (K %d, N %d)", m.K, m.N);
+    auto tokens = [&](int box) { return encode(&xmap, m.xq, m.K, m.T, m.ldxq, box); };
+    cudaError_t e;
+    const int sms = sm_count(), pairs = (m.N + 2 * kCh - 1) / (2 * kCh) * ((m.T + 255) / 256);
+    static const char *force = getenv("Q8_FORCE");
+    const int bt = force ? atoi(force) : pairs >= sms / 2 ? 512 : m.T <= 16 ? 16 : m.T <= 32 ? 32 : m.T <= 64 ? 64 : 128;
     const int tiles = (m.N + kCh - 1) / kCh * ((m.T + bt - 1) / bt), nk = (m.K + kKb - 1) / kKb;
     a.split = 1;
-    while (a.split < 8 && a.split * 2 <= nk / 2 && tiles * a.split * 2 <= 296) a.split *= 2;
-    CUtensorMap wmap, xmap;
-    if (!encode(&wmap, m.wq, m.K, m.N, m.ldw, kCh) || !encode(&xmap, m.xq, m.K, m.T, m.ldxq, bt))
-        return fail(HFQ_ERR_CUDA, "8-bit product: tensor map encoding failed (T %d, K %d, N %d)", m.T, m.K, m.N);
-    cudaError_t e = bt == 16   ? launch_tile<16>(a, wmap, xmap, s)
+    const int most = bt < 64 ? 2 * sms : sms;
+    while (a.split < 8 && a.split * 2 <= nk / 2 && tiles * a.split * 2 <= most) a.split *= 2;
+    static const char *fsplit = getenv("Q8_SPLIT");
+    if (fsplit) a.split = atoi(fsplit);
+    if (!tokens(bt == 512 ? 128 : bt == 256 ? 64 : bt)) return fail(HFQ_ERR_CUDA, "8-bit product: tensor map encoding failed (K %d, T %d)", m.K, m.T);
+    e = bt == 512 ? launch_pair<256>(a, wmap, xmap, s)
+        : bt == 256 ? launch_pair<128>(a, wmap, xmap, s)
+        : bt == 16   ? launch_tile<16>(a, wmap, xmap, s)
                     : bt == 32 ? launch_tile<32>(a, wmap, xmap, s)
                     : bt == 64 ? launch_tile<64>(a, wmap, xmap, s)
                                : launch_tile<128>(a, wmap, xmap, s);

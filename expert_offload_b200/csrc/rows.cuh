@@ -35,11 +35,6 @@ __device__ __forceinline__ void expand8(const Raw8 &r, float (&v)[8])
         v[i] = BF16 ? __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) : __uint_as_float(w[i]);
 }
 
-__device__ __forceinline__ uint32_t two_bf16(float lo, float hi)
-{
-    return (uint32_t)float_to_bf16_bits(lo) | (uint32_t)float_to_bf16_bits(hi) << 16;
-}
-
 // Rounds v to bf16 (as a float).
 __device__ __forceinline__ float round_bf16(float v) { return bf16_bits_to_float(float_to_bf16_bits(v)); }
 
