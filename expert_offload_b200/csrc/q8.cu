@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(512) quantize_kernel(const QuantArgs a)
 }
 
 // -------------------------------------------------- few tokens: dot products
-// Up to eight tokens read every weight once and do little with it, so the
+// One or two tokens read every weight once and do little with it, so the
 // product is bound by the weights' bytes; CUDA cores (dp4a) keep up, and one
 // launch does it all: while a warp's first weights are on their way, its block
 // quantises the tokens into shared memory.
@@ -251,20 +251,18 @@ cudaError_t launch_dot(const DotArgs &a, int smem, cudaStream_t s)
     return cudaGetLastError();
 }
 
-// Tokens that the dot kernel takes.
-constexpr int kDotTokens = 8;
-bool takes_dot(int T) { return T <= kDotTokens; }
+// One or two tokens and few weights: the dot kernel's short start wins (2.9 us
+// against 4 us and more for one token of 2048 x 1024); with more of either the
+// tensor cores' stream of weights does (17 us against 30 at 8192 x 8192).
+bool takes_dot(int T, int K, int N) { return T <= 2 && (long long)K * N * T <= (4 << 20); }
 
 hfq_status run_dot(const DotArgs &a, cudaStream_t s)
 {
     const int kp = (a.m.K + 511) / 512 * 512;
     const bool wide = a.m.N > 2 * kDotWarps * 148;         // channels for two a warp on every SM
-    const int T = a.m.T;
     cudaError_t e;
-    if (T == 1) e = wide ? launch_dot<1, 2>(a, kp, s) : launch_dot<1, 1>(a, kp, s);
-    else if (T == 2) e = wide ? launch_dot<2, 2>(a, 2 * kp, s) : launch_dot<2, 1>(a, 2 * kp, s);
-    else if (T <= 4) e = wide ? launch_dot<4, 2>(a, 4 * kp, s) : launch_dot<4, 1>(a, 4 * kp, s);
-    else e = wide ? launch_dot<8, 2>(a, 8 * kp, s) : launch_dot<8, 1>(a, 8 * kp, s);
+    if (a.m.T == 1) e = wide ? launch_dot<1, 2>(a, kp, s) : launch_dot<1, 1>(a, kp, s);
+    else e = wide ? launch_dot<2, 2>(a, 2 * kp, s) : launch_dot<2, 1>(a, 2 * kp, s);
     if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "8-bit product launch: %s", cudaGetErrorString(e));
     return HFQ_OK;
 }
@@ -303,14 +301,14 @@ hfq_status q8_matmul(const int8_t *xq, int ldxq, const float *xs, int T, int K, 
     if (misaligned(xs, HFQ_F32)) return fail(HFQ_ERR_ALIGN, "q8_matmul: xs must be 4-byte aligned");
     const Q8Mat m{xq, wq, xs, ws, y, ldxq ? (size_t)ldxq : round16(K), ldw ? (size_t)ldw : round16(K),
                   (size_t)(ldy ? ldy : N), T, K, N, y_dtype == HFQ_BF16};
-    st = takes_dot(T) ? run_dot(DotArgs{m, nullptr, 0, 0, 0}, (cudaStream_t)stream)
+    st = takes_dot(T, K, N) ? run_dot(DotArgs{m, nullptr, 0, 0, 0}, (cudaStream_t)stream)
                       : launch_q8_tc(m, false, (cudaStream_t)stream);
     return st ? st : ok();
 }
 
 size_t q8_linear_workspace_bytes(int T, int K, int N)
 {
-    if (T < 1 || K < 1 || N < 1 || takes_dot(T)) return 0;
+    if (T < 1 || K < 1 || N < 1 || T <= kQ8FusedTokens) return 0;
     return ((size_t)T * round16(K) + 255) / 256 * 256 + (size_t)T * sizeof(float);
 }
 
@@ -332,8 +330,10 @@ hfq_status q8_linear(const void *x, hfq_dtype x_dtype, int ldx, int T, int K, co
     cudaStream_t s = (cudaStream_t)stream;
     Q8Mat m{nullptr, wq, nullptr, ws, y, round16(K), ldw ? (size_t)ldw : round16(K), (size_t)(ldy ? ldy : N), T, K, N,
             y_dtype == HFQ_BF16};
-    if (takes_dot(T)) {
+    if (takes_dot(T, K, N)) {
         st = run_dot(DotArgs{m, x, ld, bf16, aligned16(x) && ld * (bf16 ? 2 : 4) % 16 == 0}, s);
+    } else if (T <= kQ8FusedTokens) {
+        st = launch_q8_fused(m, x, bf16, ld, s);
     } else {
         int8_t *xq = static_cast<int8_t *>(workspace);
         float *xs = reinterpret_cast<float *>(xq + ((size_t)T * round16(K) + 255) / 256 * 256);

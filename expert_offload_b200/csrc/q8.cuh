@@ -21,6 +21,9 @@ __device__ __forceinline__ float q8_value(int acc, float xs, float ws) { return 
 // Tensor-core product (q8_tc.cu).  `chained`: the kernel before it on the
 // stream is the quantiser of xq, which started after everything that wrote wq.
 hfq_status launch_q8_tc(const Q8Mat &a, bool chained, cudaStream_t s);
+// The same for up to 8 tokens that come as they are, quantised on the way.
+constexpr int kQ8FusedTokens = 8;
+hfq_status launch_q8_fused(const Q8Mat &a, const void *x, bool x_bf16, size_t ldx, cudaStream_t s);
 // Status word of its bounded waits on the current device; clears it.
 hfq_status q8_status(cudaStream_t s);
 

@@ -11,13 +11,16 @@
 
 #include "ptx.cuh"
 #include "q8.cuh"
+#include "rows.cuh"
 
 namespace hfq {
 namespace {
 
 constexpr int kCh = 128;                  // channels of a tile (MMA M)
 constexpr int kKb = 128;                  // K of a stage: one swizzled row of 128 bytes, 4 MMAs
-constexpr int kThr = 192;                 // TMA warp, MMA warp, 4 warps for tensor memory
+constexpr int kMaxStages = 12;            // of a tile kernel's ring
+constexpr int kSmemFull = 222 * 1024;     // dynamic shared memory of a CTA that has an SM to itself
+constexpr int kSmemHalf = 110 * 1024;     // of one of two
 
 __device__ unsigned g_status;             // HFQ_ERR_TIMEOUT after a wait ran out
 
@@ -45,9 +48,14 @@ __device__ __forceinline__ uint32_t cluster_rank()
     return r;
 }
 
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ void cluster_sync()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 __device__ __forceinline__ uint32_t map_rank(uint32_t smem, uint32_t rank)
@@ -63,14 +71,27 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, int a, int b, int c
                  : "memory");
 }
 
+// A word into another CTA's shared memory, counted on its barrier `bar`.
+__device__ __forceinline__ void st_async(uint32_t addr, uint32_t v, uint32_t bar)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(addr), "r"(v),
+                 "r"(bar)
+                 : "memory");
+}
+
 // Work that another kernel launched before this one on the stream may still
 // be doing: waits until it has finished and its writes are visible.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 struct Args {
     Q8Mat m;
+    const void *x;                        // fused: the tokens as they are, rows ldx elements apart
+    size_t ldx;
+    int x_bf16, x_vec;
     long long timeout_ns;
+    int stages;                           // of the tile kernel's ring
     int split;                            // CTAs of a cluster, each with a share of K (two stages at least)
+    int share;                            // stages of K that a CTA of the cluster takes at most
     int chained;                          // weights may be read before the dependency wait
     int hook;                             // test hook: the MMA warp waits for an arrival that never comes
 };
@@ -168,28 +189,42 @@ __device__ __forceinline__ void store_columns(const Q8Mat &m, int t0, int n, int
 // a share of K each and add their sums through distributed shared memory
 // (integers, so the order does not matter): CTA r of the cluster owns channels
 // [128 r / split, 128 (r + 1) / split) of the tile.
-template <int BT>
+//
+// FUSED (up to 8 tokens, one tile of them): no quantised rows come in.  While
+// the weights are on their way, eight warps find each token's largest magnitude
+// (every CTA of its share of K, the shares' maxima exchanged through the
+// cluster), and write the CTA's share of the quantised rows where the MMAs read
+// them, in the 128-byte swizzle that a TMA load would have given them.  One
+// launch, and x is read from L2 by every channel tile, which is cheaper than
+// a kernel before this one: 16 tokens of a 2048 x 1024 product took 5.7 us with
+// the quantiser before them.
+constexpr int kFew = 16;                  // tokens of its tile
+constexpr int kShare = 24;                // its stages of K: 48 KB of quantised tokens
+constexpr int kQuantWarps = 8;
+
+template <int BT, bool FUSED>
 struct TileCfg {
-    static constexpr int kStages = 4;
-    static constexpr int kA = kCh * kKb, kB = BT * kKb, kStage = kA + kB;
+    static constexpr int kA = kCh * kKb, kB = BT * kKb, kStage = FUSED ? kA : kA + kB;
     static constexpr int kExch = kCh * BT * 4;                       // bytes of the exchange
-    static constexpr int kSmem = 1024 + kStages * kStage;
-    static constexpr int kSmemSplit = kSmem + kExch;
+    static constexpr int kThr = FUSED ? 64 + 32 * kQuantWarps : 192; // TMA warp, MMA warp, the others
     static constexpr uint32_t kCols = BT < 32 ? 32 : BT;             // tensor-memory columns
 };
 
-template <int BT>
-__global__ void __launch_bounds__(kThr)
+template <int BT, bool FUSED>
+__global__ void __launch_bounds__(TileCfg<BT, FUSED>::kThr)
 q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap)
 {
-    using C = TileCfg<BT>;
+    using C = TileCfg<BT, FUSED>;
     extern __shared__ uint8_t raw[];
     uint8_t *buf = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t full[C::kStages], empty[C::kStages], done, never;
+    uint8_t *xbuf = buf + a.stages * C::kStage;                      // FUSED: [share][kB]
+    uint8_t *ebuf = xbuf + (FUSED ? a.share * C::kB : 0);            // the exchange
+    __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done, never, xready, amax_bar;
     __shared__ __align__(16) float xs_of[4][32];
+    __shared__ uint32_t top_in[8][kFew], top[kFew];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, stages = a.stages;
     const Q8Mat &m = a.m;
     const int rank = a.split > 1 ? (int)cluster_rank() : 0;
     const int n0 = (int)(blockIdx.x / a.split) * kCh, t0 = (int)blockIdx.y * BT;
@@ -197,13 +232,18 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
     const int c0 = (int)((long long)nk * rank / a.split), c1 = (int)((long long)nk * (rank + 1) / a.split);
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < C::kStages; ++i) {
+        for (int i = 0; i < stages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
         mbar_init(&done, 1);
         mbar_init(&never, 1);
+        if (FUSED) {
+            mbar_init(&xready, 1);
+            mbar_init(&amax_bar, 1);
+        }
         fence_mbar_init();
+        if (FUSED && a.split > 1) mbar_arrive_expect_tx(&amax_bar, (uint32_t)(a.split * m.T * 4));
         abort_flag = 0;
     }
     if (warp == 1) {
@@ -213,89 +253,144 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
+    if (a.split > 1) cluster_arrive();    // waited for before this CTA touches another's shared memory
     const uint32_t tmem = tmem_base;
     volatile int *abortp = &abort_flag;
 
-    if (warp == 0 && lane == 0) {
-        int issued = 0;
-        bool waited = false;
-        if (!a.chained) {
-            grid_dependency_wait();
-            waited = true;
-        }
-        for (int c = c0; c < c1; ++c, ++issued) {
-            const int s = issued % C::kStages;
-            if (issued >= C::kStages &&
-                !wait_bar(&empty[s], (uint32_t)(issued / C::kStages - 1) & 1u, a.timeout_ns, abortp))
-                break;
-            uint8_t *dst = buf + s * C::kStage;
-            mbar_arrive_expect_tx(&full[s], C::kStage);
-            tma_load_2d(dst, &wmap, c * kKb, n0, &full[s]);
-            if (!waited && (issued == C::kStages - 1 || c == c1 - 1)) {
-                // the first stages' weights are on their way: now the tokens
+    if (warp == 0) {
+        if (lane == 0) {
+            int issued = 0, s = -1, round = 0;               // issued = round * stages + s + 1
+            bool waited = false;
+            if (!a.chained) {
                 grid_dependency_wait();
                 waited = true;
-                for (int j = 0; j <= issued; ++j)
-                    tma_load_2d(buf + j * C::kStage + C::kA, &xmap, (c0 + j) * kKb, t0, &full[j]);
-            } else if (waited)
-                tma_load_2d(dst + C::kA, &xmap, c * kKb, t0, &full[s]);
+            }
+            for (int c = c0; c < c1; ++c, ++issued) {
+                if (++s == stages) s = 0, ++round;
+                if (round > 0 && !wait_bar(&empty[s], (uint32_t)(round - 1) & 1u, a.timeout_ns, abortp)) break;
+                uint8_t *dst = buf + s * C::kStage;
+                mbar_arrive_expect_tx(&full[s], C::kStage);
+                tma_load_2d(dst, &wmap, c * kKb, n0, &full[s]);
+                if (FUSED) continue;
+                if (!waited && (issued == stages - 1 || c == c1 - 1)) {
+                    // the first stages' weights are on their way: now the tokens
+                    grid_dependency_wait();
+                    waited = true;
+                    for (int j = 0; j <= issued; ++j)
+                        tma_load_2d(buf + j * C::kStage + C::kA, &xmap, (c0 + j) * kKb, t0, &full[j]);
+                } else if (waited)
+                    tma_load_2d(dst + C::kA, &xmap, c * kKb, t0, &full[s]);
+            }
+            // every copy has landed before the CTA may end
+            for (int i = max(0, issued - stages); i < issued; ++i)
+                wait_bar(&full[i % stages], (uint32_t)(i / stages) & 1u, a.timeout_ns, nullptr);
         }
-        // every copy has landed before the CTA may end
-        for (int i = max(0, issued - C::kStages); i < issued; ++i)
-            wait_bar(&full[i % C::kStages], (uint32_t)(i / C::kStages) & 1u, a.timeout_ns, nullptr);
-    } else if (warp == 1 && lane == 0) {
-        bool ok = !a.hook || wait_bar(&never, 0u, a.timeout_ns, abortp);
-        for (int i = 0; ok && i < c1 - c0; ++i) {
-            const int s = i % C::kStages;
-            if (!(ok = wait_bar(&full[s], (uint32_t)(i / C::kStages) & 1u, a.timeout_ns, abortp))) break;
-            tc_fence_after_sync();
-            const uint64_t ad = umma_desc_sw128(buf + s * C::kStage), bd = umma_desc_sw128(buf + s * C::kStage + C::kA);
+        __syncwarp();
+        if (a.split > 1) cluster_wait();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            bool ok = !a.hook || wait_bar(&never, 0u, a.timeout_ns, abortp);
+            if (FUSED && ok) ok = wait_bar(&xready, 0u, a.timeout_ns, abortp);
+            for (int i = 0, s = 0, round = 0; ok && i < c1 - c0; ++i) {
+                if (!(ok = wait_bar(&full[s], (uint32_t)round & 1u, a.timeout_ns, abortp))) break;
+                tc_fence_after_sync();
+                const uint64_t ad = umma_desc_sw128(buf + s * C::kStage);
+                const uint64_t bd = umma_desc_sw128(FUSED ? xbuf + i * C::kB : buf + s * C::kStage + C::kA);
 #pragma unroll
-            for (int k = 0; k < kKb / 32; ++k)
-                umma_i8(tmem, ad + 2 * k, bd + 2 * k, idesc_i8(kCh, BT), i > 0 || k > 0);
-            umma_commit(&empty[s]);
+                for (int k = 0; k < kKb / 32; ++k)
+                    umma_i8(tmem, ad + 2 * k, bd + 2 * k, idesc_i8(kCh, BT), i > 0 || k > 0);
+                umma_commit(&empty[s]);
+                if (++s == stages) s = 0, ++round;
+            }
+            umma_commit(&done);
+            wait_bar(&done, 0u, a.timeout_ns, nullptr);      // after an abort, too, no MMA may still run
         }
-        umma_commit(&done);
-        wait_bar(&done, 0u, a.timeout_ns, nullptr);        // after an abort, too, no MMA may still run
-    }
-    __syncwarp();
-
-    // the sums: warp w reads lanes 32 (w % 4) .. + 31
-    if (warp >= 2) {
-        const bool ok = wait_bar(&done, 0u, a.timeout_ns, abortp);
-        tc_fence_after_sync();
-        const int ch = (warp & 3) * 32 + lane, n = n0 + ch;
-        const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const int tv = min(BT, m.T - t0);
-        if (ok) {
-            if (a.split == 1) {
-                grid_dependency_wait();                    // xs comes from the kernel before, too
-                const bool pairs = m.y_bf16 && m.ldy % 2 == 0 && ((uintptr_t)m.y & 3) == 0;
-                const float ws = n < m.N ? m.ws[n] : 0.0f;
-#pragma unroll 1
-                for (int col = 0; col < tv; col += 32) {
-                    int v[32];
-                    tmem_ld32(trow + col, v);
-                    __syncwarp();                            // the last columns' scales have been read
-                    xs_of[warp - 2][lane] = col + lane < tv ? __ldg(m.xs + t0 + col + lane) : 0.0f;
-                    __syncwarp();
-                    store_columns(m, t0 + col, n, lane, pairs, ws, xs_of[warp - 2], v);
+        __syncwarp();
+        if (a.split > 1) cluster_wait();
+    } else {
+        if (a.split > 1) cluster_wait();
+        if (FUSED) {
+            const int k0 = c0 * kKb, k1 = min(m.K, c1 * kKb);
+            for (int t = warp - 2; t < m.T; t += kQuantWarps) {
+                const void *row = row_at(a.x, a.x_bf16, (size_t)t * a.ldx);
+                uint32_t big = 0;
+                for (int k = k0 + 8 * lane; k < k1; k += 256) {
+                    float v[8];
+                    load8(row, a.x_bf16, a.x_vec, k, k1, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) big = max(big, abs_bits(v[e]));
                 }
-            } else {
-                // four tokens of a channel are 16 bytes, next to those of the next
-                // channel: a warp's store is one run of 512 bytes for each owner
-                const int own = kCh / a.split, owner = ch / own;
-                const uint32_t mine = smem_u32(buf + C::kStages * C::kStage) +
-                                      (uint32_t)(rank * own * BT * 4 + (ch - owner * own) * 16);
-                const uint32_t dst = map_rank(mine, (uint32_t)owner);
+                big = __reduce_max_sync(0xffffffffu, big);
+                if (a.split == 1) {
+                    if (lane == 0) top[t] = big;
+                } else if (lane < a.split)
+                    st_async(map_rank(smem_u32(&top_in[rank][t]), (uint32_t)lane), big,
+                             map_rank(smem_u32(&amax_bar), (uint32_t)lane));
+            }
+            __syncwarp();
+            if (a.split > 1) {
+                wait_bar(&amax_bar, 0u, a.timeout_ns, abortp);
+                for (int t = warp - 2; t < m.T; t += kQuantWarps) {
+                    const uint32_t big = __reduce_max_sync(0xffffffffu, lane < a.split ? top_in[lane][t] : 0u);
+                    if (lane == 0) top[t] = big;
+                }
+                __syncwarp();
+            }
+            for (int t = warp - 2; t < m.T; t += kQuantWarps) {
+                const void *row = row_at(a.x, a.x_bf16, (size_t)t * a.ldx);
+                const RowQuant<true> qb(top[t]);
+                const RowQuant<false> qf(top[t]);
+                for (int k = k0 + 8 * lane; k < k1; k += 256) {
+                    float v[8];
+                    load8(row, a.x_bf16, a.x_vec, k, k1, v);
+                    // row t of the tile, 16-byte piece (k / 16) % 8 at its swizzled place
+                    uint8_t *at = xbuf + (k - k0) / kKb * C::kB + t * kKb + ((((k >> 4) & 7) ^ (t & 7)) << 4) + (k & 8);
+                    *reinterpret_cast<uint2 *>(at) = a.x_bf16 ? qb(v) : qf(v);
+                }
+            }
+            fence_proxy_async_smem();                        // the MMAs read through the async proxy
+            asm volatile("bar.sync 1, %0;" ::"n"(32 * kQuantWarps) : "memory");
+            if (threadIdx.x == 64) mbar_arrive(&xready);
+        }
+        if (warp < 6) {
+            // the sums: warp w reads lanes 32 (w % 4) .. + 31
+            const bool ok = wait_bar(&done, 0u, a.timeout_ns, abortp);
+            __syncwarp();
+            tc_fence_after_sync();
+            const int ch = (warp & 3) * 32 + lane, n = n0 + ch;
+            const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+            const int tv = min(BT, m.T - t0);
+            if (__all_sync(0xffffffffu, ok)) {
+                if (a.split == 1) {
+                    if (!FUSED) grid_dependency_wait();      // xs comes from the kernel before, too
+                    const bool pairs = m.y_bf16 && m.ldy % 2 == 0 && ((uintptr_t)m.y & 3) == 0;
+                    const float ws = n < m.N ? m.ws[n] : 0.0f;
 #pragma unroll 1
-                for (int col = 0; col < tv; col += 32) {
-                    int v[32];
-                    tmem_ld32(trow + col, v);
+                    for (int col = 0; col < tv; col += 32) {
+                        int v[32];
+                        tmem_ld32(trow + col, v);
+                        __syncwarp();                        // the last columns' scales have been read
+                        xs_of[warp - 2][lane] = col + lane >= tv ? 0.0f
+                                                : FUSED          ? row_scale(top[lane])
+                                                                 : __ldg(m.xs + t0 + col + lane);
+                        __syncwarp();
+                        store_columns(m, t0 + col, n, lane, pairs, ws, xs_of[warp - 2], v);
+                    }
+                } else {
+                    // four tokens of a channel are 16 bytes, next to those of the next
+                    // channel: a warp's store is one run of 512 bytes for each owner
+                    const int own = kCh / a.split, owner = ch / own;
+                    const uint32_t mine = smem_u32(ebuf) + (uint32_t)(rank * own * BT * 4 + (ch - owner * own) * 16);
+                    const uint32_t dst = map_rank(mine, (uint32_t)owner);
+#pragma unroll 1
+                    for (int col = 0; col < tv; col += 32) {
+                        int v[32];
+                        tmem_ld32(trow + col, v);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        if (col + j < tv)
-                            st_cluster_v4(dst + (uint32_t)((col + j) / 4 * own * 16), v[j], v[j + 1], v[j + 2], v[j + 3]);
+                        for (int j = 0; j < 32; j += 4)
+                            if (col + j < tv)
+                                st_cluster_v4(dst + (uint32_t)((col + j) / 4 * own * 16), v[j], v[j + 1], v[j + 2], v[j + 3]);
+                    }
                 }
             }
         }
@@ -303,22 +398,24 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
     if (a.split > 1) {
         __syncwarp();
         cluster_sync();
-        grid_dependency_wait();
+        if (!FUSED) grid_dependency_wait();
         const int own = kCh / a.split, tv = min(BT, m.T - t0);
-        const int4 *part = reinterpret_cast<const int4 *>(buf + C::kStages * C::kStage);
-        for (int i = threadIdx.x; i < own * ((tv + 3) / 4); i += kThr) {
-            const int q = i / own, c = i - q * own, n = n0 + rank * own + c, t = t0 + 4 * q;
+        const int4 *part = reinterpret_cast<const int4 *>(ebuf);
+        for (int i = threadIdx.x; i < own * ((tv + 3) / 4); i += C::kThr) {
+            const int q = i / own, c = i - q * own, n = n0 + rank * own + c;
             if (n >= m.N) continue;
-            int4 sum = make_int4(0, 0, 0, 0);
+            int sum[4] = {0, 0, 0, 0};
             for (int r = 0; r < a.split; ++r) {
                 const int4 p = part[r * own * (BT / 4) + i];
-                sum.x += p.x, sum.y += p.y, sum.z += p.z, sum.w += p.w;
+                sum[0] += p.x, sum[1] += p.y, sum[2] += p.z, sum[3] += p.w;
             }
             const float ws = __ldg(m.ws + n);
-            store_y(m, t, n, q8_value(sum.x, __ldg(m.xs + t), ws));
-            if (t + 1 < m.T) store_y(m, t + 1, n, q8_value(sum.y, __ldg(m.xs + t + 1), ws));
-            if (t + 2 < m.T) store_y(m, t + 2, n, q8_value(sum.z, __ldg(m.xs + t + 2), ws));
-            if (t + 3 < m.T) store_y(m, t + 3, n, q8_value(sum.w, __ldg(m.xs + t + 3), ws));
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (4 * q + j < tv) {
+                    const int t = t0 + 4 * q + j;
+                    store_y(m, t, n, q8_value(sum[j], FUSED ? row_scale(top[4 * q + j]) : __ldg(m.xs + t), ws));
+                }
         }
     }
     tc_fence_before_sync();
@@ -328,11 +425,11 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
 }
 
 // ------------------------------------------------ large products: CTA pairs
-// A pair of CTAs (cta_group::2) works on tiles of 256 channels x BT tokens: each
+// A pair of CTAs (cta_group::2) works on tiles of 256 channels x 256 tokens: each
 // CTA brings its 128 channels and half of the tokens, the leader's MMAs read
 // both shared memories, and each CTA's tensor memory gets its own channels'
-// sums of all BT tokens.  A stage of 128 K bytes is thus 32 KB a CTA for 512
-// clocks of the tensor pipe (BT = 256), 64 bytes a clock, where a CTA alone
+// sums of all 256 tokens.  A stage of 128 K bytes is thus 32 KB a CTA for 512
+// clocks of the tensor pipe, 64 bytes a clock, where a CTA alone
 // would need 96: more than L2 delivers to every SM.
 //
 // Persistent: a pair walks tiles with two accumulator buffers, so the
@@ -341,12 +438,12 @@ constexpr int kEpiWarps = 8;
 constexpr int kPairThr = 64 + 32 * kEpiWarps;
 constexpr int kEpiParts = kEpiWarps / 4;  // of a tile's columns, each for four warps
 
-template <int BT>
 struct PairCfg {
-    static constexpr int kA = kCh * kKb, kB = BT / 2 * kKb, kStage = kA + kB;
-    static constexpr int kStages = 196608 / kStage;                  // 6 of 32 KB, 8 of 24 KB
+    static constexpr int kBT = 256;                                  // tokens of a tile
+    static constexpr int kA = kCh * kKb, kB = kBT / 2 * kKb, kStage = kA + kB;
+    static constexpr int kStages = 6;
     static constexpr int kSmem = 1024 + kStages * kStage;
-    static constexpr uint32_t kCols = 2 * BT;
+    static constexpr uint32_t kCols = 2 * kBT;
 };
 
 __device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -394,11 +491,11 @@ __device__ __forceinline__ void tile_of(int i, int ct, int tt, int &c, int &t)
     c = c0 + r - t * w;
 }
 
-template <int BT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThr)
 q8_pair_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap)
 {
-    using C = PairCfg<BT>;
+    using C = PairCfg;
+    constexpr int BT = C::kBT;
     extern __shared__ uint8_t raw[];
     uint8_t *buf = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], never;
@@ -550,17 +647,24 @@ bool encode(CUtensorMap *map, const int8_t *base, int K, int rows, size_t ld, in
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BT>
+template <int BT, bool FUSED>
 cudaError_t launch_tile(Args a, const CUtensorMap &wmap, const CUtensorMap &xmap, cudaStream_t s)
 {
-    using C = TileCfg<BT>;
-    const int smem = a.split > 1 ? C::kSmemSplit : C::kSmem;
-    cudaError_t e = cudaFuncSetAttribute(q8_tile_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemSplit);
+    using C = TileCfg<BT, FUSED>;
+    const cudaError_t e = cudaFuncSetAttribute(q8_tile_kernel<BT, FUSED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kSmemFull);
     if (e != cudaSuccess) return e;
+    // as many stages as K has, and as fit with one CTA or two on an SM (two for
+    // clusters: eight CTAs that need an SM each do not find room in every GPC)
+    const int tiles = (a.m.N + kCh - 1) / kCh * ((a.m.T + BT - 1) / BT), nk = (a.m.K + kKb - 1) / kKb;
+    a.share = (nk + a.split - 1) / a.split;
+    const int fixed = 1024 + (FUSED ? a.share * C::kB : 0) + (a.split > 1 ? C::kExch : 0);
+    const int room = (!FUSED && a.split == 1 && tiles <= sm_count() ? kSmemFull : kSmemHalf) - fixed;
+    a.stages = std::min({kMaxStages, a.share, std::max(2, room / C::kStage)});
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.m.N + kCh - 1) / kCh * a.split, (a.m.T + BT - 1) / BT);
-    cfg.blockDim = dim3(kThr);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(C::kThr);
+    cfg.dynamicSmemBytes = fixed + a.stages * C::kStage;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -570,14 +674,14 @@ cudaError_t launch_tile(Args a, const CUtensorMap &wmap, const CUtensorMap &xmap
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.chained ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, q8_tile_kernel<BT>, a, wmap, xmap);
+    return cudaLaunchKernelEx(&cfg, q8_tile_kernel<BT, FUSED>, a, wmap, xmap);
 }
 
-template <int BT>
 cudaError_t launch_pair(const Args &a, const CUtensorMap &wmap, const CUtensorMap &xmap, cudaStream_t s)
 {
-    using C = PairCfg<BT>;
-    cudaError_t e = cudaFuncSetAttribute(q8_pair_kernel<BT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    using C = PairCfg;
+    constexpr int BT = C::kBT;
+    cudaError_t e = cudaFuncSetAttribute(q8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     const int tiles = (a.m.N + 2 * kCh - 1) / (2 * kCh) * ((a.m.T + BT - 1) / BT);
     cudaLaunchConfig_t cfg = {};
@@ -590,40 +694,74 @@ cudaError_t launch_pair(const Args &a, const CUtensorMap &wmap, const CUtensorMa
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.chained ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, q8_pair_kernel<BT>, a, wmap, xmap);
+    return cudaLaunchKernelEx(&cfg, q8_pair_kernel, a, wmap, xmap);
 }
 
 }  // namespace
 
+// CTAs of a cluster for tiles of bt tokens.  Splitting K shortens each CTA's
+// run through it (0.27 us a stage) and puts more of the memory system to work,
+// up to two CTAs on an SM; it costs the exchange of the sums (about 1.5 us for
+// 64 tokens), so a tile of many tokens is split only if K is long: with tiles
+// on half of the SMs, 16 stages lose (12.1 us for 11.4 at 128 x 2048 x 8192),
+// 64 gain (23.8 for 28.7 at 512 x 8192 x 2048).
+static int split_of(int bt, int tiles, int nk)
+{
+    const int sms = sm_count(), least = bt == kFew ? 1 : 2;
+    if (bt > 32 && nk < (2 * tiles > sms ? 32 : 8)) return 1;
+    int split = 1;
+    while (split < 8 && nk >= 2 * split * least && tiles * split * 2 <= 2 * sms) split *= 2;
+    return split;
+}
+
+hfq_status launch_q8_fused(const Q8Mat &m, const void *x, bool x_bf16, size_t ldx, cudaStream_t s)
+{
+    if (!encode_fn()) return fail(HFQ_ERR_CUDA, "8-bit product: cuTensorMapEncodeTiled unavailable");
+    Args a = {};
+    a.m = m;
+    a.x = x;
+    a.ldx = ldx;
+    a.x_bf16 = x_bf16;
+    a.x_vec = aligned16(x) && ldx * (x_bf16 ? 2 : 4) % 16 == 0;
+    a.timeout_ns = option_wait_timeout_ns();
+    a.hook = option_take_extra_arrivals();
+    const int nk = (m.K + kKb - 1) / kKb;
+    a.split = split_of(kFew, (m.N + kCh - 1) / kCh, nk);
+    while ((nk + a.split - 1) / a.split > kShare) a.split *= 2;      // at most 128 stages: 8
+    CUtensorMap wmap;
+    if (!encode(&wmap, m.wq, m.K, m.N, m.ldw, kCh))
+        return fail(HFQ_ERR_CUDA, "8-bit product: tensor map encoding failed (K %d, N %d)", m.K, m.N);
+    cudaError_t e = launch_tile<kFew, true>(a, wmap, wmap, s);
+    if (e == cudaSuccess) e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "8-bit product launch: %s", cudaGetErrorString(e));
+    return HFQ_OK;
+}
+
 hfq_status launch_q8_tc(const Q8Mat &m, bool chained, cudaStream_t s)
 {
     if (!encode_fn()) return fail(HFQ_ERR_CUDA, "8-bit product: cuTensorMapEncodeTiled unavailable");
-    Args a;
+    Args a = {};
     a.m = m;
     a.timeout_ns = option_wait_timeout_ns();
     a.chained = chained;
     a.hook = option_take_extra_arrivals();
+    // Tiles of 16 and 32 tokens where they take all of them.  For more, CTA pairs
+    // once their 256 x 256 tiles fill most of the SMs (35.5 us against 37.9 with
+    // tiles of 128 at 512 x 8192 x 8192), else tiles of 64 as long as there are no
+    // more than two for each SM, else of 128.
+    const int sms = sm_count(), nk = (m.K + kKb - 1) / kKb;
+    const int ct = (m.N + kCh - 1) / kCh, pairs = (m.N + 2 * kCh - 1) / (2 * kCh) * ((m.T + 255) / 256);
+    const bool pair = m.T > 64 && 7 * sms / 16 <= pairs;
+    const int bt = m.T <= 16 ? 16 : m.T <= 32 ? 32 : ct * ((m.T + 63) / 64) <= 2 * sms ? 64 : 128;
     CUtensorMap wmap, xmap;
-    if (!encode(&wmap, m.wq, m.K, m.N, m.ldw, kCh))
-        return fail(HFQ_ERR_CUDA, "8-bit product: tensor map encoding failed (K %d, N %d)", m.K, m.N);
-    auto tokens = [&](int box) { return encode(&xmap, m.xq, m.K, m.T, m.ldxq, box); };
-    cudaError_t e;
-    const int sms = sm_count(), pairs = (m.N + 2 * kCh - 1) / (2 * kCh) * ((m.T + 255) / 256);
-    static const char *force = getenv("Q8_FORCE");
-    const int bt = force ? atoi(force) : pairs >= sms / 2 ? 512 : m.T <= 16 ? 16 : m.T <= 32 ? 32 : m.T <= 64 ? 64 : 128;
-    const int tiles = (m.N + kCh - 1) / kCh * ((m.T + bt - 1) / bt), nk = (m.K + kKb - 1) / kKb;
-    a.split = 1;
-    const int most = bt < 64 ? 2 * sms : sms;
-    while (a.split < 8 && a.split * 2 <= nk / 2 && tiles * a.split * 2 <= most) a.split *= 2;
-    static const char *fsplit = getenv("Q8_SPLIT");
-    if (fsplit) a.split = atoi(fsplit);
-    if (!tokens(bt == 512 ? 128 : bt == 256 ? 64 : bt)) return fail(HFQ_ERR_CUDA, "8-bit product: tensor map encoding failed (K %d, T %d)", m.K, m.T);
-    e = bt == 512 ? launch_pair<256>(a, wmap, xmap, s)
-        : bt == 256 ? launch_pair<128>(a, wmap, xmap, s)
-        : bt == 16   ? launch_tile<16>(a, wmap, xmap, s)
-                    : bt == 32 ? launch_tile<32>(a, wmap, xmap, s)
-                    : bt == 64 ? launch_tile<64>(a, wmap, xmap, s)
-                               : launch_tile<128>(a, wmap, xmap, s);
+    if (!encode(&wmap, m.wq, m.K, m.N, m.ldw, kCh) || !encode(&xmap, m.xq, m.K, m.T, m.ldxq, pair ? 128 : bt))
+        return fail(HFQ_ERR_CUDA, "8-bit product: tensor map encoding failed (T %d, K %d, N %d)", m.T, m.K, m.N);
+    a.split = split_of(bt, ct * ((m.T + bt - 1) / bt), nk);
+    cudaError_t e = pair       ? launch_pair(a, wmap, xmap, s)
+                    : bt == 16 ? launch_tile<16, false>(a, wmap, xmap, s)
+                    : bt == 32 ? launch_tile<32, false>(a, wmap, xmap, s)
+                    : bt == 64 ? launch_tile<64, false>(a, wmap, xmap, s)
+                               : launch_tile<128, false>(a, wmap, xmap, s);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "8-bit product launch: %s", cudaGetErrorString(e));
     return HFQ_OK;
