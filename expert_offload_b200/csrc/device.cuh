@@ -148,6 +148,8 @@ hfq_status launch_tc(const hfq4_layer &L, const void *x, bool x_f32, int T, int 
 // Status word of the allocation-free forward's array on the current device
 // (noalloc.cu); hfq_workspace_status(NULL, 0, stream) returns it.
 hfq_status noalloc_status(cudaStream_t s);
+// Reads and clears a device status word that is not part of a workspace (noalloc.cu).
+hfq_status take_status(void *word_dev, const char *who, cudaStream_t s);
 
 // Library options (hfq_set_option).
 long long option_wait_timeout_ns();

@@ -53,6 +53,21 @@ hfq_status scratch_address(void **out)
 
 }  // namespace
 
+// Reads and clears a status word that is not part of a workspace.
+hfq_status take_status(void *word_dev, const char *who, cudaStream_t s)
+{
+    unsigned word = 0;
+    cudaError_t e = cudaMemcpyAsync(&word, word_dev, sizeof word, cudaMemcpyDeviceToHost, s);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    if (e == cudaSuccess && word) {
+        e = cudaMemsetAsync(word_dev, 0, sizeof word, s);
+        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+    }
+    if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
+    if (word) return fail((hfq_status)(int)word, "a device-side wait of %s ran out (status %d)", who, (int)word);
+    return ok();
+}
+
 // hfq_workspace_status(NULL, 0, stream): the status word of this device's
 // array.  HFQ_OK when no call has run on the device yet.  After an error the
 // array's control block is cleared, as a workspace's would be.
@@ -66,8 +81,8 @@ hfq_status noalloc_status(cudaStream_t s)
         std::lock_guard<std::mutex> g(g_mu);
         if (dev >= 0 && dev < kMaxDevices) scratch = g_scratch_ptr[dev];
     }
-    const hfq_status q8 = q8_status(s);
-    if (q8) return q8;
+    hfq_status st = q8_status(s);
+    if (st) return st;
     if (!scratch) return ok();
     unsigned word = 0;
     e = cudaMemcpyAsync(&word, scratch, sizeof word, cudaMemcpyDeviceToHost, s);
@@ -77,10 +92,10 @@ hfq_status noalloc_status(cudaStream_t s)
     e = cudaMemsetAsync(scratch, 0, stack_ctl_bytes(), s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "clearing the scratch: %s", cudaGetErrorString(e));
-    const int st = (int)word;
+    st = (hfq_status)(int)word;
     if (st == HFQ_ERR_ARG)
         return fail(HFQ_ERR_ARG, "the allocation-free forward found an invalid expert id (status %d)", st);
-    return fail((hfq_status)st, "a device-side wait of the allocation-free forward ran out (status %d)", st);
+    return fail(st, "a device-side wait of the allocation-free forward ran out (status %d)", st);
 }
 
 }  // namespace hfq

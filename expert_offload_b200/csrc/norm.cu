@@ -2,15 +2,22 @@
 // norm before the next one.
 //
 // One block of threads holds a row in registers from its first read to its
-// last write: y, y2 and x are read once, x' and xn written once, and the two
-// (three with the 8-bit output) sums over the row go through shared memory.
-// Bound by memory: at bf16 streams and an f32 block output 20 bytes an element.
+// last write: y, y2, x and the gate are read once, x' and xn written once, and
+// the two (three with the 8-bit output) reductions over the row go through
+// shared memory.  Bound by memory: at a bf16 stream and an f32 block output 20
+// bytes an element, so what counts is how many bytes are on their way.
+//
+// Everything a row needs is requested before anything is used, so that a row
+// costs one trip to memory.
+#include <algorithm>
 #include <cfloat>
 
 #include "rows.cuh"
 
 namespace hfq {
 namespace {
+
+constexpr int kPacked = 8;
 
 struct Args {
     const void *x, *y, *y2, *w_post, *w_pre;
@@ -20,15 +27,39 @@ struct Args {
     float *xq_scale;
     size_t ldx, ldy;
     int T, H;
+    int packed;                           // kPacked rows of one warp each in a block
     int w_bf16, xn_bf16;
     int gate_kind, gate_sigmoid;
-    float eps, w_offset, alpha, beta;
+    float inv_h, eps, w_offset, alpha, beta;
 };
 
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
+// expf within 2 ulp, the reciprocal within 1.
+__device__ __forceinline__ float sigmoid(float v)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-v)));
+    return r;
+}
+
+// 32 bytes in one access.
+__device__ __forceinline__ void load32(const void *p, uint32_t (&w)[8])
+{
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+
+__device__ __forceinline__ void store32(void *p, const float (&v)[8])
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+}
 
 // The elements of thread `tid` of a row: with VEC chunks of 8 neighbours, 8
 // elements apart from the next thread's; else single elements, a block apart.
+// Elements are kept as they lie in memory (8 words a chunk: of bf16 chunks
+// four are used) until they are needed, so that no load waits for another.
 template <bool VEC, int NV>
 struct Row {
     int nt, tid, H;
@@ -40,216 +71,308 @@ struct Row {
     __device__ __forceinline__ bool in(int c, int i) const { return at(c, i) < H; }
 
     template <bool BF16>
-    __device__ __forceinline__ void load(const void *p, size_t base, float (&v)[NV][8]) const
+    __device__ __forceinline__ void load(const void *p, size_t base, uint32_t (&w)[NV][8]) const
     {
-        if (VEC) {
-            Raw8 r[NV];
 #pragma unroll
-            for (int c = 0; c < NV; ++c)
-                if (in(c, 0)) r[c] = load_raw8<BF16>(p, base + at(c, 0));
+        for (int c = 0; c < NV; ++c)
 #pragma unroll
-            for (int c = 0; c < NV; ++c) {
-                if (in(c, 0)) expand8<BF16>(r[c], v[c]);
-                else
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[c][i] = 0.0f;
-            }
-        } else {
-#pragma unroll
-            for (int c = 0; c < NV; ++c)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[c][i] = 0.0f;
-                    if (in(c, i))
-                        v[c][i] = BF16 ? bf16_bits_to_float(static_cast<const uint16_t *>(p)[base + at(c, i)])
-                                       : static_cast<const float *>(p)[base + at(c, i)];
-                }
-        }
-    }
-
-    __device__ __forceinline__ void store(void *p, size_t base, bool bf16, const float (&v)[NV][8]) const
-    {
+            for (int i = 0; i < 8; ++i) w[c][i] = 0;
 #pragma unroll
         for (int c = 0; c < NV; ++c) {
             if (VEC) {
                 if (!in(c, 0)) continue;
-                if (bf16) {
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + base + at(c, 0)) =
-                        make_uint4(two_bf16(v[c][0], v[c][1]), two_bf16(v[c][2], v[c][3]),
-                                   two_bf16(v[c][4], v[c][5]), two_bf16(v[c][6], v[c][7]));
-                } else {
-                    float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + base + at(c, 0));
-                    q[0] = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
-                    q[1] = make_float4(v[c][4], v[c][5], v[c][6], v[c][7]);
-                }
+                if (BF16) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + base + at(c, 0));
+                    w[c][0] = v.x, w[c][1] = v.y, w[c][2] = v.z, w[c][3] = v.w;
+                } else
+                    load32(static_cast<const float *>(p) + base + at(c, 0), w[c]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (in(c, i)) {
-                        if (bf16) static_cast<uint16_t *>(p)[base + at(c, i)] = float_to_bf16_bits(v[c][i]);
-                        else static_cast<float *>(p)[base + at(c, i)] = v[c][i];
+                    if (in(c, i))
+                        w[c][i] = BF16 ? static_cast<const uint16_t *>(p)[base + at(c, i)]
+                                       : static_cast<const uint32_t *>(p)[base + at(c, i)];
+            }
+        }
+    }
+
+    __device__ __forceinline__ void load_as(const void *p, size_t base, bool bf16, uint32_t (&w)[NV][8]) const
+    {
+        if (bf16) load<true>(p, base, w);
+        else load<false>(p, base, w);
+    }
+
+    template <bool BF16>
+    static __device__ __forceinline__ float value(const uint32_t (&w)[8], int i)
+    {
+        if (!BF16) return __uint_as_float(w[i]);
+        if (!VEC) return __uint_as_float(w[i] << 16);
+        return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+
+    // Writes the row rounded to its type and leaves the rounded values in v.
+    template <bool ROUNDED>
+    __device__ __forceinline__ void store(void *p, size_t base, bool bf16, float (&v)[NV][8]) const
+    {
+#pragma unroll
+        for (int c = 0; c < NV; ++c) {
+            if (bf16) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[i] = two_bf16(v[c][2 * i], v[c][2 * i + 1]);
+                    if (ROUNDED) {
+                        v[c][2 * i] = __uint_as_float(w[i] << 16);
+                        v[c][2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
                     }
+                }
+                if (!p) continue;
+                if (VEC) {
+                    if (in(c, 0))
+                        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + base + at(c, 0)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (in(c, i))
+                            static_cast<uint16_t *>(p)[base + at(c, i)] = (uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2]);
+                }
+            } else if (p) {
+                if (VEC) {
+                    if (in(c, 0)) store32(static_cast<float *>(p) + base + at(c, 0), v[c]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (in(c, i)) static_cast<float *>(p)[base + at(c, i)] = v[c][i];
+                }
             }
         }
     }
 };
 
-// Sum over the block in a fixed order; every thread gets it.
-__device__ __forceinline__ float block_sum(float v, float *red, int nt)
-{
-    v = warp_sum(v);
-    if (nt == 32) return v;
-    const int lane = threadIdx.x & 31;
-    __syncthreads();                                 // the last sum's words have been read
-    if (lane == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return warp_sum(lane < nt / 32 ? red[lane] : 0.0f);
-}
+// Reductions over the block in a fixed order; every thread gets the result.
+// Each has words of its own for even and odd rows, so one barrier is enough:
+// a thread that is a barrier ahead writes words that nobody reads any more.
+constexpr int kReds = 5;
+constexpr int kMaxWarps = 16;
 
-__device__ __forceinline__ uint32_t block_max(uint32_t v, float *red, int nt)
-{
-    v = __reduce_max_sync(0xffffffffu, v);
-    if (nt == 32) return v;
-    const int lane = threadIdx.x & 31;
-    __syncthreads();
-    if (lane == 0) red[threadIdx.x >> 5] = __uint_as_float(v);
-    __syncthreads();
-    return __reduce_max_sync(0xffffffffu, lane < nt / 32 ? __float_as_uint(red[lane]) : 0u);
-}
+struct Reds {
+    float (*red)[kMaxWarps];              // [kReds] of this row; words of absent warps are 0
+    int nt;
 
-// 1 / rms of a row as two factors, r and f: v * f * r.  f is 1 unless the sum
-// of squares leaves the f32 range; then the row is summed again at 2^-64.
-template <int NV>
-__device__ __forceinline__ float2 inv_rms(const float (&v)[NV][8], int H, float eps, float *red, int nt)
-{
-    float s = 0.0f;
-#pragma unroll
-    for (int c = 0; c < NV; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(v[c][i], v[c][i], s);
-    s = block_sum(s, red, nt);
-    if (s <= FLT_MAX) return make_float2(1.0f, 1.0f / sqrtf(s / (float)H + eps));
-    s = 0.0f;
-#pragma unroll
-    for (int c = 0; c < NV; ++c)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float u = v[c][i] * 0x1p-64f;
-            s = fmaf(u, u, s);
+    __device__ __forceinline__ float sum(int which, float v) const
+    {
+        v = warp_sum(v);
+        if (nt == 32) return v;
+        if ((threadIdx.x & 31) == 0) red[which][threadIdx.x >> 5] = v;
+        __syncthreads();
+        const float4 *q = reinterpret_cast<const float4 *>(red[which]);
+        const float4 a = q[0], b = q[1];
+        float t = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
+        if (nt > 256) {
+            const float4 c = q[2], d = q[3];
+            t += ((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w));
         }
-    s = block_sum(s, red, nt);
-    return make_float2(0x1p-64f, 1.0f / sqrtf(s / (float)H + eps * 0x1p-128f));
-}
+        return t;
+    }
 
-template <bool VEC, int NV, bool XB, bool YB>
-__global__ void __launch_bounds__(NV * 256) norm_kernel(const Args a)
-{
-    __shared__ float red[32];
-    const int nt = blockDim.x;
-    const Row<VEC, NV> row{nt, (int)threadIdx.x, a.H};
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
-        const size_t bx = (size_t)t * a.ldx, by = (size_t)t * a.ldy, b0 = (size_t)t * a.H;
-        float x[NV][8], b[NV][8], w[NV][8];
-        row.template load<XB>(a.x, bx, x);
-        if (a.y) {
-            row.template load<YB>(a.y, by, b);
-            if (a.y2) {
-                const float g = a.y2_gate ? sigmoid(a.y2_gate[t]) : 1.0f;
-                row.template load<YB>(a.y2, by, w);
+    __device__ __forceinline__ uint32_t max(int which, uint32_t v) const
+    {
+        v = __reduce_max_sync(0xffffffffu, v);
+        if (nt == 32) return v;
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) red[which][threadIdx.x >> 5] = __uint_as_float(v);
+        __syncthreads();
+        return __reduce_max_sync(0xffffffffu, __float_as_uint(red[which][lane & (kMaxWarps - 1)]));
+    }
+
+    // 1 / sqrt(mean(v^2) + eps).  Where the sum of squares leaves the f32 range
+    // the row is scaled by 2^-64 (in v, too) and summed again.
+    template <int NV>
+    __device__ __forceinline__ float inv_rms(int which, float (&v)[NV][8], float inv_h, float eps) const
+    {
+        float s = 0.0f;
 #pragma unroll
-                for (int c = 0; c < NV; ++c)
+        for (int c = 0; c < NV; ++c)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) b[c][i] = fmaf(g, w[c][i], b[c][i]);
-            }
-            if (a.w_post) {
-                const float2 r = inv_rms<NV>(b, a.H, a.eps, red, nt);
-                if (a.w_bf16) row.template load<true>(a.w_post, 0, w);
-                else row.template load<false>(a.w_post, 0, w);
-#pragma unroll
-                for (int c = 0; c < NV; ++c)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) b[c][i] = b[c][i] * r.x * r.y * (w[c][i] + a.w_offset);
-            }
-            if (a.gate_kind == HFQ_GATE_TOKEN) {
-                const float g = a.gate_sigmoid ? sigmoid(a.gate[t]) : a.gate[t];
-#pragma unroll
-                for (int c = 0; c < NV; ++c)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) b[c][i] *= g;
-            } else if (a.gate_kind != HFQ_GATE_NONE) {
-                row.template load<false>(a.gate, a.gate_kind == HFQ_GATE_FULL ? b0 : 0, w);
-#pragma unroll
-                for (int c = 0; c < NV; ++c)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) b[c][i] *= a.gate_sigmoid ? sigmoid(w[c][i]) : w[c][i];
-            }
+            for (int i = 0; i < 8; ++i) s = fmaf(v[c][i], v[c][i], s);
+        s = sum(which, s);
+        if (!(s <= FLT_MAX)) {
+            s = 0.0f;
 #pragma unroll
             for (int c = 0; c < NV; ++c)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float v = fmaf(a.beta, b[c][i], a.alpha * x[c][i]);
-                    // elements behind the row stay 0, whatever the gate's value made of them
-                    x[c][i] = row.in(c, i) ? (XB ? round_bf16(v) : v) : 0.0f;
+                    v[c][i] *= 0x1p-64f;
+                    s = fmaf(v[c][i], v[c][i], s);
                 }
+            s = sum(which + 1, s);
+            eps *= 0x1p-128f;
         }
-        if (a.x_out) row.store(a.x_out, bx, XB, x);
-        if (!a.xn && !a.xq) continue;
-        const float2 r = inv_rms<NV>(x, a.H, a.eps, red, nt);
-        if (a.w_pre) {
-            if (a.w_bf16) row.template load<true>(a.w_pre, 0, w);
-            else row.template load<false>(a.w_pre, 0, w);
-#pragma unroll
-            for (int c = 0; c < NV; ++c)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[c][i] += a.w_offset;
-        } else {
-#pragma unroll
-            for (int c = 0; c < NV; ++c)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[c][i] = 1.0f;
-        }
-#pragma unroll
-        for (int c = 0; c < NV; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[c][i] = x[c][i] * r.x * r.y * w[c][i];
-        if (a.xn) row.store(a.xn, b0, a.xn_bf16, x);
-        if (!a.xq) continue;
-        uint32_t top = 0;
+        float r;
+        asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(fmaf(s, inv_h, eps)));       // within 2^-22.9
+        return r;
+    }
+};
+
+// The two gates of a token.
+struct TokenGates {
+    float y2, gate;
+};
+
+__device__ __forceinline__ TokenGates load_gates(const Args &a, int t)
+{
+    return {a.y2_gate ? a.y2_gate[t] : 0.0f, a.gate_kind == HFQ_GATE_TOKEN ? a.gate[t] : 0.0f};
+}
+
+// One row, from its raw elements to its outputs.  The weights are the same for
+// every row: they are read where they are used, mostly from L1, and held no
+// longer, because registers decide how many rows an SM works on at once.
+template <bool VEC, int NV, bool XB, bool YB>
+__device__ __forceinline__ void do_row(const Args &a, const Row<VEC, NV> &row, const Reds &red, int t,
+                                       const uint32_t (&rx)[NV][8], const uint32_t (&ry)[NV][8],
+                                       const uint32_t (&ry2)[NV][8], const uint32_t (&rg)[NV][8],
+                                       const TokenGates &tg)
+{
+    using R = Row<VEC, NV>;
+    float x[NV][8];
+    if (a.y) {
+        float b[NV][8];
+        const float g2 = a.y2_gate ? sigmoid(tg.y2) : 1.0f;
 #pragma unroll
         for (int c = 0; c < NV; ++c)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                if (a.xn_bf16) x[c][i] = round_bf16(x[c][i]);
-                if (row.in(c, i)) top = max(top, abs_bits(x[c][i]));
+                b[c][i] = R::template value<YB>(ry[c], i);
+                if (a.y2) b[c][i] = fmaf(g2, R::template value<YB>(ry2[c], i), b[c][i]);
             }
-        top = block_max(top, red, nt);
-        const RowQuant<true> qb(top);
-        const RowQuant<false> qf(top);
-        const size_t ldq = round16(a.H);
-        int8_t *out = a.xq + (size_t)t * ldq;
+        if (a.w_post) {
+            const float r = red.template inv_rms<NV>(0, b, a.inv_h, a.eps);
+            uint32_t w[NV][8];
+            row.load_as(a.w_post, 0, a.w_bf16, w);
 #pragma unroll
-        for (int c = 0; c < NV; ++c) {
-            const uint2 w = a.xn_bf16 ? qb(x[c]) : qf(x[c]);
-            if (VEC) {
-                if (row.in(c, 0)) *reinterpret_cast<uint2 *>(out + row.at(c, 0)) = w;
-            } else {
+            for (int c = 0; c < NV; ++c)
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    if (row.in(c, i)) out[row.at(c, i)] = (int8_t)((i < 4 ? w.x : w.y) >> 8 * (i & 3));
-            }
+                    b[c][i] = b[c][i] * r *
+                              ((a.w_bf16 ? R::template value<true>(w[c], i) : R::template value<false>(w[c], i)) +
+                               a.w_offset);
         }
-        if (threadIdx.x < ldq - a.H) out[a.H + threadIdx.x] = 0;
-        if (threadIdx.x == 0) a.xq_scale[t] = row_scale(top);
+        if (a.gate_kind == HFQ_GATE_TOKEN) {
+            const float g = a.gate_sigmoid ? sigmoid(tg.gate) : tg.gate;
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) b[c][i] *= g;
+        } else if (a.gate_kind != HFQ_GATE_NONE) {
+            const bool full = a.gate_kind == HFQ_GATE_FULL;
+            uint32_t w[NV][8];
+            if (!full) row.template load<false>(a.gate, 0, w);
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float g = __uint_as_float(full ? rg[c][i] : w[c][i]);
+                    b[c][i] *= a.gate_sigmoid ? sigmoid(g) : g;
+                }
+        }
+#pragma unroll
+        for (int c = 0; c < NV; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[c][i] = fmaf(a.beta, b[c][i], a.alpha * R::template value<XB>(rx[c], i));
+                // elements behind the row stay 0, whatever the gate's value made of them
+                if (!row.in(c, VEC ? 0 : i)) x[c][i] = 0.0f;
+            }
+        row.template store<XB>(a.x_out, (size_t)t * a.ldx, XB, x);
+    } else {
+#pragma unroll
+        for (int c = 0; c < NV; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[c][i] = R::template value<XB>(rx[c], i);
+        if (a.x_out) row.template store<false>(a.x_out, (size_t)t * a.ldx, XB, x);
     }
+    if (!a.xn && !a.xq) return;
+    const float r = red.template inv_rms<NV>(2, x, a.inv_h, a.eps);
+    uint32_t w[NV][8];
+    if (a.w_pre) row.load_as(a.w_pre, 0, a.w_bf16, w);
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[c][i] *= r;
+            if (a.w_pre)
+                x[c][i] *= (a.w_bf16 ? R::template value<true>(w[c], i) : R::template value<false>(w[c], i)) + a.w_offset;
+        }
+    if (!a.xq) {
+        row.template store<false>(a.xn, (size_t)t * a.H, a.xn_bf16, x);
+        return;
+    }
+    row.template store<true>(a.xn, (size_t)t * a.H, a.xn_bf16, x);
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < NV; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (row.in(c, i)) top = max(top, abs_bits(x[c][i]));
+    top = red.max(4, top);
+    const RowQuant<true> qb(top);
+    const RowQuant<false> qf(top);
+    const size_t ldq = round16(a.H);
+    int8_t *out = a.xq + (size_t)t * ldq;
+#pragma unroll
+    for (int c = 0; c < NV; ++c) {
+        const uint2 q = a.xn_bf16 ? qb(x[c]) : qf(x[c]);
+        if (VEC) {
+            if (row.in(c, 0)) *reinterpret_cast<uint2 *>(out + row.at(c, 0)) = q;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (row.in(c, i)) out[row.at(c, i)] = (int8_t)((i < 4 ? q.x : q.y) >> 8 * (i & 3));
+        }
+    }
+    if (row.tid < (int)ldq - a.H) out[a.H + row.tid] = 0;
+    if (row.tid == 0) a.xq_scale[t] = row_scale(top);
+}
+
+// Registers are held down for the sake of rows at work: 8192 rows of 2048 (bf16
+// stream, two f32 branches, 235 MB) take 40.8 us with five blocks of 256 threads
+// on an SM, 44 with four, 50.6 with the weights held in registers from the start;
+// 2048 rows of 8192 with a full gate (201 MB) take 45.5 us with two blocks of
+// 512 and 61.9 with one.  A ring of rows in shared memory, filled by bulk copies
+// ahead of persistent blocks, was slower (52 and 72 us): what a row waits for is
+// its two reductions, and more rows at once hide those best.
+template <bool VEC, int NV, bool XB, bool YB>
+__global__ void __launch_bounds__(NV * 256, NV > 1 ? 2 : VEC ? 5 : 3) norm_kernel(const Args a)
+{
+    __shared__ __align__(16) float red[kReds][kMaxWarps];
+    // rows of one warp share blocks; others have one of their own
+    const int nt = a.packed ? 32 : blockDim.x, sub = a.packed ? threadIdx.x >> 5 : 0;
+    const int t = a.packed ? blockIdx.x * kPacked + sub : blockIdx.x;
+    if (t >= a.T) return;
+    const Row<VEC, NV> row{nt, (int)threadIdx.x - sub * nt, a.H};
+    uint32_t x[NV][8], y[NV][8], y2[NV][8], g[NV][8];
+    row.template load<XB>(a.x, (size_t)t * a.ldx, x);
+    if (a.y) row.template load<YB>(a.y, (size_t)t * a.ldy, y);
+    if (a.y2) row.template load<YB>(a.y2, (size_t)t * a.ldy, y2);
+    if (a.gate_kind == HFQ_GATE_FULL) row.template load<false>(a.gate, (size_t)t * a.H, g);
+    const TokenGates tg = load_gates(a, t);
+    if (nt > 32) {
+        for (int i = threadIdx.x; i < kReds * kMaxWarps; i += nt) red[0][i] = 0.0f;
+        __syncthreads();
+    }
+    do_row<VEC, NV, XB, YB>(a, row, Reds{red, nt}, t, x, y, y2, g, tg);
 }
 
 template <bool VEC, int NV>
-void launch(const Args &a, bool xb, bool yb, int nt, cudaStream_t s)
+void launch(Args a, bool xb, bool yb, int nt, cudaStream_t s)
 {
-    if (xb && yb) norm_kernel<VEC, NV, true, true><<<a.T, nt, 0, s>>>(a);
-    else if (xb) norm_kernel<VEC, NV, true, false><<<a.T, nt, 0, s>>>(a);
-    else if (yb) norm_kernel<VEC, NV, false, true><<<a.T, nt, 0, s>>>(a);
-    else norm_kernel<VEC, NV, false, false><<<a.T, nt, 0, s>>>(a);
+    a.packed = nt == 32 && a.T > 148;
+    const int rows = a.packed ? kPacked : 1, grid = (a.T + rows - 1) / rows, block = nt * rows;
+    if (xb && yb) norm_kernel<VEC, NV, true, true><<<grid, block, 0, s>>>(a);
+    else if (xb) norm_kernel<VEC, NV, true, false><<<grid, block, 0, s>>>(a);
+    else if (yb) norm_kernel<VEC, NV, false, true><<<grid, block, 0, s>>>(a);
+    else norm_kernel<VEC, NV, false, false><<<grid, block, 0, s>>>(a);
 }
 
 bool finite(float v) { return v >= -FLT_MAX && v <= FLT_MAX; }
@@ -297,15 +420,17 @@ extern "C" hfq_status moe_norm_residual(const moe_norm_rule *rule, int T, int H,
     a.ldx = ldx ? ldx : H; a.ldy = ldy ? ldy : H; a.T = T; a.H = H;
     a.w_bf16 = rule->w_dtype == HFQ_BF16; a.xn_bf16 = xn_dtype == HFQ_BF16;
     a.gate_kind = rule->gate_kind; a.gate_sigmoid = rule->gate_act == HFQ_GATE_SIGMOID;
+    a.inv_h = 1.0f / (float)H;
     a.eps = rule->eps; a.w_offset = rule->w_offset; a.alpha = rule->residual_scale; a.beta = rule->branch_scale;
 
-    // 16-byte loads need rows of whole 8-element chunks at 16-byte addresses
+    // a chunk of 8 elements is one access: 16 bytes of bf16, 32 of f32
     auto rows16 = [](const void *p, size_t ld, int d) {
-        return !p || (aligned16(p) && ld * (d == HFQ_BF16 ? 2 : 4) % 16 == 0);
+        const size_t unit = d == HFQ_BF16 ? 16 : 32;
+        return !p || ((uintptr_t)p % unit == 0 && ld * (d == HFQ_BF16 ? 2 : 4) % unit == 0);
     };
     const bool vec = H % 8 == 0 && rows16(x, a.ldx, x_dtype) && rows16(x_out, a.ldx, x_dtype) &&
                      rows16(y, a.ldy, y_dtype) && rows16(y2, a.ldy, y_dtype) && rows16(xn, H, xn_dtype) &&
-                     rows16(a.w_post, 8, HFQ_F32) && rows16(a.w_pre, 8, HFQ_F32) &&
+                     rows16(a.w_post, 8, rule->w_dtype) && rows16(a.w_pre, 8, rule->w_dtype) &&
                      rows16(a.gate_kind >= HFQ_GATE_CHANNEL ? gate : nullptr, 8, HFQ_F32);
     const bool xb = x_dtype == HFQ_BF16, yb = y_dtype == HFQ_BF16;
     cudaStream_t s = (cudaStream_t)stream;

@@ -770,17 +770,9 @@ hfq_status launch_q8_tc(const Q8Mat &m, bool chained, cudaStream_t s)
 hfq_status q8_status(cudaStream_t s)
 {
     void *p = nullptr;
-    cudaError_t e = cudaGetSymbolAddress(&p, g_status);
-    unsigned word = 0;
-    if (e == cudaSuccess) e = cudaMemcpyAsync(&word, p, sizeof word, cudaMemcpyDeviceToHost, s);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    if (e == cudaSuccess && word) {
-        e = cudaMemsetAsync(p, 0, sizeof word, s);
-        if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-    }
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_status);
     if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
-    if (word) return fail((hfq_status)(int)word, "a device-side wait of an 8-bit product ran out (status %d)", (int)word);
-    return ok();
+    return take_status(p, "an 8-bit product", s);
 }
 
 }  // namespace hfq
