@@ -3,9 +3,24 @@
 // expert's pairs.
 //
 // One warp decides a token.  Lane l owns a run of consecutive experts of one
-// group (32 / n_groups lanes, rounded down to a power of two, share a group),
-// so the order of the lanes is the order of the experts: of equal keys the
-// lowest lane's, and in a lane the first, is the lowest expert.
+// group (32 / n_groups lanes, rounded down to a power of two, share a group).
+//
+// The order of the experts is that of 64-bit sums of score and bias, but nearly
+// always 32 bits are enough to see it:
+//   1. scores c in f32, with a bound on their error;
+//   2. the k-th largest of the lanes' maxima bounds the k-th largest c from
+//      below, so everything not below it (less the bound) is a candidate;
+//      typically k + 2 to k + 4 of 256;
+//   3. the candidates, one a lane, are ranked by comparing all pairs.
+// If two candidates lie within their errors of each other the lanes take their
+// candidates' scores again in 64 bits and rank those; the groups' standing is
+// settled the same way from each group's two best.  Where there are more than
+// 32 candidates (many equal scores) or fewer than k live experts the token is
+// decided in 64 bits from the start (select64).
+// Without a bias the logits decide, which are exact as they are.
+//
+// Bound by instructions: one token of 512 experts is about 600 of a warp.
+#include <algorithm>
 #include <cfloat>
 
 #include "device.cuh"
@@ -13,20 +28,25 @@
 namespace hfq {
 namespace {
 
-constexpr int kWarps = 8;        // warps of a block
-constexpr int kTok = 32;         // tokens of a block with lists: one chunk of the pair lists
+constexpr int kMaxCand = 32;     // candidates: one a lane
+constexpr int kListWarps = 16;   // warps of a block with lists
+constexpr int kTokMax = 64;      // tokens of a block with lists, at most: one chunk of the pair lists
+constexpr int kScanChunks = 256; // chunks that the placing blocks add up by themselves
 
 struct Args {
     const void *logits;
     const float *bias;
     int32_t *idx;
     float *wts;
-    int32_t *hist;               // [chunks][E], or null without the lists
+    uint16_t *hist;              // [chunks][E], or null without the lists
+    int32_t *cnt, *off, *perm;   // one block alone: it writes the lists itself
     size_t ld;
     int T, E, k;
     int n_groups, size, topk_groups, group_top;
     int tpl, run;                // lanes of a group, experts of a lane
+    int tok;                     // tokens of a block (lists)
     int bf16, sigmoid, renorm;
+    int vec;                     // runs are whole 16-byte pieces of the logits
     float scale;
 };
 
@@ -82,11 +102,18 @@ __device__ __forceinline__ float weight_of(const Args &a, float l, int lane, flo
     return sum > 0.0f ? s / sum * a.scale : 0.0f;
 }
 
+struct Slot {
+    int e;
+    float l;
+};
+
 // Routes one token in 64 bits: returns in lane j < k the expert of slot j and
-// its logit.
+// its logit.  (The 64-bit paths read the token's logits again: taking the
+// caller's registers would put those in memory for every token.)
 template <int N>
-__device__ void select64(const Args &a, size_t row, int lane, float m, int &my_e, float &my_l)
+__device__ __noinline__ Slot select64(const Args &a, size_t row, int lane, float m)
 {
+    Slot slot{0, -INFINITY};
     const int grp = lane / a.tpl, part = lane - grp * a.tpl;
     const int e0 = grp * a.size + part * a.run;
     const int n = grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0;
@@ -156,58 +183,431 @@ __device__ void select64(const Args &a, size_t row, int lane, float m, int &my_e
             }
         const int e = __shfl_sync(0xffffffffu, e0 + at, win);
         lw = __shfl_sync(0xffffffffu, lw, win);
-        if (lane == j) { my_e = e; my_l = lw; }
+        if (lane == j) slot = Slot{e, lw};
     }
+    return slot;
+}
+
+// Largest of the lanes' values (redux of an order-preserving map; -inf is below
+// all others, NaN does not occur).
+__device__ __forceinline__ float redux_max(float v)
+{
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    const uint32_t m = __reduce_max_sync(0xffffffffu, b >> 31 ? ~b : b | 0x80000000u);
+    return __uint_as_float(m >> 31 ? m & 0x7fffffffu : ~m);
+}
+
+// Selection score of expert e in 64 bits, from its logit.
+__device__ __forceinline__ double score64(const Args &a, float l, int e, float m, double inv_z)
+{
+    if (!(l > -INFINITY)) return -INFINITY;
+    const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)m) * inv_z;
+    return a.bias ? s + (double)a.bias[e] : s;
+}
+
+__device__ __forceinline__ float rcp_approx(float v)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// 1 / sum of exp(l - m) over the token's experts, in 64 bits.
+__device__ __noinline__ double inv_sum64(const Args &a, size_t row, int lane, float m)
+{
+    double z = 0.0;
+    for (int e = lane; e < a.E; e += 32) {
+        const float l = read_logit(a, row, e);
+        if (l > -INFINITY) z += exp((double)l - (double)m);
+    }
+    return 1.0 / sum64(z);
+}
+
+// Selection score of expert e in f32 (see select_token for its error).
+__device__ __forceinline__ float score32(const Args &a, float l, float b, float m, float inv_z)
+{
+    const float s = a.sigmoid ? rcp_approx(1.0f + __expf(-l)) : __expf(l - m) * inv_z;
+    return l > -INFINITY ? s + b : -INFINITY;
+}
+
+struct Cand {                    // of a warp
+    float c[kMaxCand], l[kMaxCand];
+    int e[kMaxCand];
+};
+
+// Which groups stay, in 64 bits: each lane takes one of the candidates for a
+// group's best two (all members not below `low`, which allows for the error of
+// them).  Returns 1 or 0 for this lane's group, -1 in all lanes if there are
+// more than 32 of them.
+template <int N>
+__device__ __noinline__ int groups64(const Args &a, size_t row, float low, int lane, float m, float zi, Cand &cand)
+{
+    const int grp = lane / a.tpl, part = lane - grp * a.tpl;
+    const int e0 = grp * a.size + part * a.run;
+    const int mine_n = grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0;
+    int n = 0;
+    for (int i = 0; i < a.run; ++i) {
+        float l = -INFINITY, c = -INFINITY;
+        if (i < mine_n) {
+            l = read_logit(a, row, e0 + i);
+            c = score32(a, l, a.bias ? a.bias[e0 + i] : 0.0f, m, zi);
+        }
+        const bool in = c > -INFINITY && c >= low;
+        const unsigned who = __ballot_sync(0xffffffffu, in);
+        const int at = n + __popc(who & ((1u << lane) - 1u));
+        if (in && at < kMaxCand) cand.l[at] = l, cand.e[at] = e0 + i;
+        n += __popc(who);
+    }
+    if (n > kMaxCand) return -1;
+    __syncwarp();
+    const double inv_z = a.sigmoid ? 1.0 : inv_sum64(a, row, lane, m);
+    const int e = lane < n ? cand.e[lane] : 0;
+    const double s = lane < n ? score64(a, cand.l[lane], e, m, inv_z) : -INFINITY;
+    const int g = lane < n ? e / a.size : -1;
+    double t1 = -INFINITY, t2 = -INFINITY;              // of group `lane`
+    for (int j = 0; j < n; ++j) {
+        const double v = __shfl_sync(0xffffffffu, s, j);
+        const int h = __shfl_sync(0xffffffffu, g, j);
+        if (h == lane) {
+            t2 = fmax(t2, fmin(t1, v));
+            t1 = fmax(t1, v);
+        }
+    }
+    const double mine = a.group_top > 1 && t2 > -INFINITY ? t1 + t2 : t1;
+    int ahead = 0;
+    for (int h = 0; h < a.n_groups; ++h) {
+        const double v = __shfl_sync(0xffffffffu, mine, h);
+        ahead += v > mine || (v == mine && h < lane);
+    }
+    const unsigned kept = __ballot_sync(0xffffffffu, lane < a.n_groups && ahead < a.topk_groups);
+    __syncwarp();
+    return grp < a.n_groups && (kept >> grp & 1u);
+}
+
+// A token's selection: in lane j < k the expert of slot j and its logit.
+// `l` are the lane's logits, `b` its biases, m and z the softmax's maximum and
+// sum (f32).
+template <int N>
+__device__ __forceinline__ Slot select_token(const Args &a, size_t row, const float (&l)[N], const float (&b)[N],
+                                             int lane, float m, float z, Cand &cand)
+{
+    constexpr float kU = 0x1p-24f;
+    const int grp = lane / a.tpl, part = lane - grp * a.tpl;
+    const int e0 = grp * a.size + part * a.run;
+    const bool scored = a.bias || (a.n_groups > 1 && a.group_top > 1);
+    // Errors, in units of 2^-24.  Sigmoid: the exponential is off by 4 and by 1.5
+    // for each unit of |l| (the product's and the constant's rounding), which a
+    // score of at most 1 / (1 + exp(|l|)) turns into less than 0.5; sum 1,
+    // reciprocal 2: under 8.  Softmax: the same for numerator and sum, 21
+    // additions of the sum, quotient 2: under 33 of the largest score 1 / z.  The
+    // bias' addition: |c|.
+    const float smax = a.sigmoid ? 1.0f : rcp_approx(z), base = kU * (a.sigmoid ? 8.0f : 36.0f * smax);
+    float c[N];                  // what experts are compared by
+    bool keep = grp < a.n_groups;
+    if (scored) {
+        float s[N];
+        const float zi = a.sigmoid ? 1.0f : smax;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            s[i] = score32(a, l[i], b[i], m, zi);
+            c[i] = a.bias ? s[i] : l[i];
+        }
+        if (a.n_groups > 1) {
+            float t1 = -INFINITY, t2 = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                t2 = fmaxf(t2, fminf(t1, s[i]));
+                t1 = fmaxf(t1, s[i]);
+            }
+            for (int o = 1; o < a.tpl; o <<= 1) {
+                const float o1 = __shfl_xor_sync(0xffffffffu, t1, o), o2 = __shfl_xor_sync(0xffffffffu, t2, o);
+                t2 = fmaxf(fminf(t1, o1), fmaxf(t2, o2));
+                t1 = fmaxf(t1, o1);
+            }
+            const bool two = a.group_top > 1 && t2 > -INFINITY;
+            const float g = grp < a.n_groups ? (two ? t1 + t2 : t1) : -INFINITY;
+            int ahead = 0;
+            for (int q = 0; q < a.n_groups; ++q) {
+                const float h = __shfl_sync(0xffffffffu, g, q * a.tpl);
+                ahead += h > g || (h == g && q < grp);
+            }
+            keep = keep && ahead < a.topk_groups;
+            if (a.topk_groups < a.n_groups) {
+                // the last group that stays and the first that does not, and how far
+                // off their sums may be
+                const float in = -redux_max(keep ? -g : -INFINITY), out = redux_max(keep ? -INFINITY : g);
+                const float off = t1 > -INFINITY ? 2.0f * fabsf(t1) + 2.0f * (two ? fabsf(t2) : 0.0f) : 0.0f;
+                const float err = 2.0f * base + kU * redux_max(off);
+                // -inf on the outside: those groups have no live expert
+                if (out > -INFINITY && !(in - out > 2.0f * err)) {
+                    const float low = (a.group_top > 1 ? (two ? t2 : t1) : t1) - 2.0f * err;
+                    const int kept = groups64<N>(a, row, low, lane, m, zi, cand);
+                    if (kept < 0) return select64<N>(a, row, lane, m);
+                    keep = kept;
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = l[i];
+        if (a.n_groups > 1) {                            // by the best logit: exact
+            float t1 = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < N; ++i) t1 = fmaxf(t1, l[i]);
+            for (int o = 1; o < a.tpl; o <<= 1) t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, o));
+            int ahead = 0;
+            for (int q = 0; q < a.n_groups; ++q) {
+                const float h = __shfl_sync(0xffffffffu, t1, q * a.tpl);
+                ahead += h > t1 || (h == t1 && q < grp);
+            }
+            keep = keep && ahead < a.topk_groups;
+        }
+    }
+    // the bound: k-th largest of the lanes' maxima (equal ones count once, which
+    // lowers it at most)
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, c[i]);
+    if (!keep) top = -INFINITY;
+    float best = 0.0f, bound = -INFINITY;
+    for (int j = 0; j < a.k; ++j) {
+        bound = redux_max(top);
+        if (j == 0) best = bound;
+        if (!(bound > -INFINITY)) break;
+        if (top == bound) top = -INFINITY;
+    }
+    const float margin = a.bias ? 2.0f * (base + kU * fmaxf(fabsf(best), bound > -INFINITY ? fabsf(bound) : 0.0f)) : 0.0f;
+    const float low = bound - 2.0f * margin;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const bool in = keep && c[i] > -INFINITY && c[i] >= low;
+        const unsigned who = __ballot_sync(0xffffffffu, in);
+        const int at = n + __popc(who & ((1u << lane) - 1u));
+        if (in && at < kMaxCand) cand.c[at] = c[i], cand.l[at] = l[i], cand.e[at] = e0 + i;
+        n += __popc(who);
+    }
+    if (n < a.k || n > kMaxCand) {
+        return select64<N>(a, row, lane, m);
+    }
+    __syncwarp();
+    const float mc = lane < n ? cand.c[lane] : -INFINITY, ml = lane < n ? cand.l[lane] : -INFINITY;
+    const int me = lane < n ? cand.e[lane] : 0x7fffffff;
+    int rank = 0;
+    bool close = false;
+    for (int j = 0; j < n; ++j) {
+        const float v = cand.c[j];
+        const int e = cand.e[j];
+        rank += v > mc || (v == mc && e < me);
+        close |= e != me && fabsf(v - mc) <= margin;
+    }
+    if (a.bias && __any_sync(0xffffffffu, close && lane < n && rank <= a.k)) {
+        const double inv_z = a.sigmoid ? 1.0 : inv_sum64(a, row, lane, m);
+        const double mine = lane < n ? score64(a, ml, me, m, inv_z) : -INFINITY;
+        rank = 0;
+        for (int j = 0; j < n; ++j) {
+            const double v = __shfl_sync(0xffffffffu, mine, j);
+            const int e = __shfl_sync(0xffffffffu, me, j);
+            rank += v > mine || (v == mine && e < me);
+        }
+    }
+    __syncwarp();                                        // all have read the candidates
+    if (lane < n && rank < a.k) cand.l[rank] = ml, cand.e[rank] = me;
+    __syncwarp();
+    const Slot slot = lane < a.k ? Slot{cand.e[lane], cand.l[lane]} : Slot{0, -INFINITY};
+    __syncwarp();
+    return slot;
+}
+
+// The lane's logits (masked ones -inf) and biases.
+template <int N>
+__device__ __forceinline__ void read_bias(const Args &a, int e0, int n, float (&b)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) b[i] = a.bias && i < n ? a.bias[e0 + i] : 0.0f;
 }
 
 template <int N>
-__global__ void __launch_bounds__(kWarps * 32) route_scored_kernel(const Args a)
+__device__ __forceinline__ void read_logits(const Args &a, size_t row, int e0, int n, const float (&b)[N], float (&l)[N])
 {
-    __shared__ int count[HFQ_MAX_EXPERTS];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int t_end = min(a.T, (int)(blockIdx.x + 1) * kTok);
-    if (a.hist) {
-        for (int e = threadIdx.x; e < a.E; e += kWarps * 32) count[e] = 0;
-        __syncthreads();
-    }
-    for (int t = blockIdx.x * kTok + warp; t < t_end; t += kWarps) {
-        const size_t row = (size_t)t * a.ld;
-        float m = 0.0f, z = 1.0f;
-        if (!a.sigmoid) {
-            m = -INFINITY;
-            for (int e = lane; e < a.E; e += 32) m = fmaxf(m, read_logit(a, row, e));
-            m = max32(m);
-            if (!(m > -INFINITY)) m = 0.0f;
-            if (!a.renorm) {
-                z = 0.0f;
-                for (int e = lane; e < a.E; e += 32) z += expf(read_logit(a, row, e) - m);
-                z = warp_sum(z);
+    if (a.vec) {                 // whole 16-byte pieces
+        if (a.bf16) {
+#pragma unroll
+            for (int i = 0; i < N; i += 8) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (i < n) v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.logits) + row + e0 + i);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    l[i + j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 4) {
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < n) v = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + row + e0 + i);
+                l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
             }
         }
-        int e = 0;
-        float l = -INFINITY;
-        select64<N>(a, row, lane, m, e, l);
-        const float w = weight_of(a, l, lane, m, z);
-        if (lane < a.k) {
-            a.idx[(size_t)t * a.k + lane] = e;
-            a.wts[(size_t)t * a.k + lane] = w;
-            if (a.hist) atomicAdd(&count[e], 1);
-        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            l[i] = i >= n    ? 0.0f
+                   : a.bf16  ? bf16_bits_to_float(static_cast<const uint16_t *>(a.logits)[row + e0 + i])
+                             : static_cast<const float *>(a.logits)[row + e0 + i];
     }
-    if (a.hist) {
-        __syncthreads();
-        for (int e = threadIdx.x; e < a.E; e += kWarps * 32) a.hist[(size_t)blockIdx.x * a.E + e] = count[e];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        l[i] = i < n && l[i] > -INFINITY && b[i] > -INFINITY ? fminf(l[i], FLT_MAX) : -INFINITY;
+}
+
+// The whole of one token; lane j < k ends with its slot j.
+template <int N>
+__device__ __forceinline__ void route_token(const Args &a, int t, int lane, const float (&b)[N], Cand &cand, int &e,
+                                            float &w)
+{
+    const int grp = lane / a.tpl, part = lane - grp * a.tpl;
+    const int e0 = grp * a.size + part * a.run;
+    const int n = grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0;
+    const size_t row = (size_t)t * a.ld;
+    float l[N];
+    read_logits(a, row, e0, n, b, l);
+    float m = 0.0f, z = 1.0f;
+    if (!a.sigmoid && (a.bias || !a.renorm || a.group_top > 1)) {
+        m = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
+        m = redux_max(m);
+        if (!(m > -INFINITY)) m = 0.0f;
+        z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) z += __expf(l[i] - m);
+        z = warp_sum(z);
+    }
+    const Slot slot = select_token<N>(a, row, l, b, lane, m, z, cand);
+    e = slot.e;
+    w = weight_of(a, slot.l, lane, m, z);
+    if (lane < a.k) {
+        a.idx[(size_t)t * a.k + lane] = e;
+        a.wts[(size_t)t * a.k + lane] = w;
     }
 }
 
+// Without lists: warps walk the tokens.
+template <int N>
+__global__ void __launch_bounds__(256) route_scored_kernel(const Args a)
+{
+    __shared__ Cand cand[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int grp = lane / a.tpl, part = lane - grp * a.tpl;
+    float b[N], w;
+    int e;
+    read_bias(a, grp * a.size + part * a.run, grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0, b);
+    for (int t = blockIdx.x * warps + warp; t < a.T; t += gridDim.x * warps) route_token<N>(a, t, lane, b, cand[warp], e, w);
+}
+
 // ------------------------------------------------------------ the pair lists
-// hist[c][e] (pairs of chunk c that go to expert e) becomes the number of such
-// pairs in the chunks before c; cnt[e] their total.  One warp for an expert.
-__global__ void lists_scan_kernel(int32_t *__restrict__ hist, int chunks, int E, int32_t *__restrict__ cnt)
+// Pairs are placed in order: `start[e]` is where expert e's next pair goes.
+// `p0` .. `p1` are handled, all threads of the block together, and start moves on.
+struct Placer {
+    int start[HFQ_MAX_EXPERTS];
+    unsigned short wcnt[kListWarps][HFQ_MAX_EXPERTS];    // zero between passes
+};
+
+__device__ __forceinline__ void place_pairs(Placer &s, const int32_t *idx, int p0, int p1, int E, int32_t *perm)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    for (int q = p0; q < p1; q += kListWarps * 32) {
+        const int p = q + tid;
+        const int e = p < p1 ? idx[p] : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, e);
+        const int rank = __popc(same & ((1u << lane) - 1u));
+        if (e >= 0 && rank == 0) s.wcnt[warp][e] = (unsigned short)__popc(same);
+        __syncthreads();
+        if (e >= 0) {
+            int pos = s.start[e] + rank;
+            for (int w = 0; w < warp; ++w) pos += s.wcnt[w][e];
+            perm[pos] = p;
+        }
+        __syncthreads();
+        for (int x = tid; x < E; x += kListWarps * 32) {
+            int n = 0;
+#pragma unroll
+            for (int w = 0; w < kListWarps; ++w) {
+                n += s.wcnt[w][x];
+                s.wcnt[w][x] = 0;
+            }
+            s.start[x] += n;
+        }
+        __syncthreads();
+    }
+}
+
+// Exclusive sums of the totals of all experts (thread e holds expert e's).
+__device__ __forceinline__ int exclusive_sum(int v, int *wsum)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int s = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += u;
+    }
+    if (lane == 31) wsum[warp] = s;
+    __syncthreads();
+    int before = 0;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    return before + s - v;
+}
+
+// With lists: a block routes a.tok tokens and counts its pairs; a block that has
+// all tokens writes the lists, too.
+template <int N>
+__global__ void __launch_bounds__(kListWarps * 32) route_count_kernel(const Args a)
+{
+    __shared__ union {
+        Cand cand[kListWarps];
+        Placer place;
+    } s;
+    __shared__ int count[HFQ_MAX_EXPERTS], wsum[kListWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int grp = lane / a.tpl, part = lane - grp * a.tpl;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    count[tid] = 0;
+    float b[N], w;
+    int e;
+    read_bias(a, grp * a.size + part * a.run, grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0, b);
+    __syncthreads();
+    const int t_end = min(a.T, ((int)blockIdx.x + 1) * a.tok);
+    for (int t = blockIdx.x * a.tok + warp; t < t_end; t += kListWarps) {
+        route_token<N>(a, t, lane, b, s.cand[warp], e, w);
+        if (lane < a.k) atomicAdd(&count[e], 1);
+    }
+    __syncthreads();
+    if (a.hist) {
+        if (tid < a.E) a.hist[(size_t)blockIdx.x * a.E + tid] = (uint16_t)count[tid];
+        return;
+    }
+    const int mine = exclusive_sum(count[tid], wsum);
+    s.place.start[tid] = mine;
+    for (int w2 = 0; w2 < kListWarps; ++w2) s.place.wcnt[w2][tid] = 0;
+    if (tid < a.E) {
+        a.cnt[tid] = count[tid];
+        a.off[tid] = mine;
+        if (tid == a.E - 1) a.off[a.E] = mine + count[tid];
+    }
+    __syncthreads();
+    place_pairs(s.place, a.idx, 0, a.T * a.k, a.E, a.perm);      // idx: written by this block
+}
+
+// Adds up the counts of many chunks, expert by expert, a warp each: base[c][e]
+// becomes the pairs of e in the chunks before c, cnt[e] the total.
+__global__ void lists_scan_kernel(const uint16_t *__restrict__ hist, int chunks, int E, int32_t *__restrict__ base,
+                                  int32_t *__restrict__ cnt)
 {
     const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (e >= E) return;
-    int base = 0;
+    int sum = 0;
     for (int c0 = 0; c0 < chunks; c0 += 32) {
         const int c = c0 + lane;
         const int v = c < chunks ? hist[(size_t)c * E + e] : 0;
@@ -217,58 +617,61 @@ __global__ void lists_scan_kernel(int32_t *__restrict__ hist, int chunks, int E,
             const int u = __shfl_up_sync(0xffffffffu, s, o);
             if (lane >= o) s += u;
         }
-        if (c < chunks) hist[(size_t)c * E + e] = base + s - v;
-        base += __shfl_sync(0xffffffffu, s, 31);
+        if (c < chunks) base[(size_t)c * E + e] = sum + s - v;
+        sum += __shfl_sync(0xffffffffu, s, 31);
     }
-    if (lane == 0) cnt[e] = base;
+    if (lane == 0) cnt[e] = sum;
 }
 
-// off = exclusive sums of cnt (block 0 writes it), then each pair of this
-// block's chunk goes to off[e] + pairs before the chunk + pairs before it in
-// the chunk.
-constexpr int kListThr = kTok * HFQ_MAX_TOPK;      // 512: one thread a pair, and one an expert
-
-__global__ void __launch_bounds__(kListThr)
-lists_place_kernel(const int32_t *__restrict__ idx, const int32_t *__restrict__ hist,
-                   const int32_t *__restrict__ cnt, int P, int per_chunk, int E, int32_t *__restrict__ off,
-                   int32_t *__restrict__ perm)
+// Places the pairs of `group` consecutive chunks.  The counts of the chunks
+// before come from base, or (base null) are added up here: all blocks read all
+// counts, 256 x 512 x 2 bytes at most, instead of a kernel between.
+__global__ void __launch_bounds__(kListWarps * 32)
+lists_place_kernel(const int32_t *__restrict__ idx, const uint16_t *__restrict__ hist, const int32_t *__restrict__ base,
+                   int chunks, int group, int P, int per_chunk, int E, int32_t *__restrict__ cnt,
+                   int32_t *__restrict__ off, int32_t *__restrict__ perm)
 {
-    __shared__ int start[HFQ_MAX_EXPERTS];
-    __shared__ int wsum[kListThr / 32];
-    __shared__ unsigned short wcnt[kListThr / 32][HFQ_MAX_EXPERTS];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int v = tid < E ? cnt[tid] : 0;
-    int s = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += u;
-    }
-    if (lane == 31) wsum[warp] = s;
-    for (int i = tid; i < kListThr / 32 * HFQ_MAX_EXPERTS; i += kListThr)
-        wcnt[i / HFQ_MAX_EXPERTS][i % HFQ_MAX_EXPERTS] = 0;
-    __syncthreads();
-    int before = 0;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
+    __shared__ Placer s;
+    __shared__ int wsum[kListWarps];
+    const int tid = threadIdx.x;
+    const int first = blockIdx.x * group;
+    for (int w = 0; w < kListWarps; ++w) s.wcnt[w][tid] = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    int before = 0, total = 0;
     if (tid < E) {
-        start[tid] = before + s - v;
-        if (blockIdx.x == 0) {
-            off[tid] = before + s - v;
-            if (tid == E - 1) off[E] = before + s;
+        if (base) {
+            before = base[(size_t)first * E + tid];
+            total = cnt[tid];
+        } else {
+            constexpr int kU = 16;
+            for (int c0 = 0; c0 < chunks; c0 += kU) {
+                int v[kU];
+#pragma unroll
+                for (int u = 0; u < kU; ++u) v[u] = c0 + u < chunks ? hist[(size_t)(c0 + u) * E + tid] : 0;
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    total += v[u];
+                    if (c0 + u < first) before += v[u];
+                }
+            }
         }
     }
-    const int p = blockIdx.x * per_chunk + tid;
-    const int e = tid < per_chunk && p < P ? idx[p] : -1;
-    const unsigned same = __match_any_sync(0xffffffffu, e);
-    const int rank = __popc(same & ((1u << lane) - 1u));
-    if (e >= 0 && rank == 0) wcnt[warp][e] = (unsigned short)__popc(same);
-    __syncthreads();
-    if (e >= 0) {
-        int pos = start[e] + hist[(size_t)blockIdx.x * E + e] + rank;
-        for (int w = 0; w < warp; ++w) pos += wcnt[w][e];
-        perm[pos] = p;
+    const int sum = exclusive_sum(total, wsum);
+    s.start[tid] = sum + before;
+    if (blockIdx.x == 0 && tid < E) {
+        off[tid] = sum;
+        if (!base) cnt[tid] = total;
+        if (tid == E - 1) off[E] = sum + total;
     }
+    __syncthreads();
+    place_pairs(s, idx, first * per_chunk, min(P, (first + group) * per_chunk), E, perm);
 }
+
+// Tokens of a chunk: one for each warp of its block until the chunks fill the
+// SMs, then up to four.
+int chunk_tokens(int T) { return T <= kListWarps * 148 ? kListWarps : T <= 2 * kListWarps * 148 ? 2 * kListWarps : kTokMax; }
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 int pow2_floor(int v)
 {
@@ -284,10 +687,14 @@ using namespace hfq;
 
 extern "C" {
 
+// Counts of the chunks, and where there are too many to be added up by the
+// placing blocks the sums of those before each.  None where one block has all
+// tokens.
 size_t moe_route_scored_workspace_bytes(int T, int E, int k)
 {
-    if (T < 1 || E < 1 || k < 1) return 0;
-    return ((size_t)T + kTok - 1) / kTok * (size_t)E * sizeof(int32_t);
+    if (T < 1 || E < 1 || k < 1 || T <= kListWarps) return 0;
+    const size_t chunks = ((size_t)T + chunk_tokens(T) - 1) / chunk_tokens(T);
+    return round256(chunks * E * sizeof(uint16_t)) + (chunks > kScanChunks ? chunks * E * sizeof(int32_t) : 0);
 }
 
 hfq_status moe_route_scored(const void *logits, hfq_dtype logits_dtype, int ld, int T, int E,
@@ -325,28 +732,61 @@ hfq_status moe_route_scored(const void *logits, hfq_dtype logits_dtype, int ld, 
     if ((words & 3) || ((uintptr_t)logits & (logits_dtype == HFQ_BF16 ? 1 : 3)))
         return fail(HFQ_ERR_ALIGN, "moe_route_scored: pointers must be aligned to their type");
     const size_t need = moe_route_scored_workspace_bytes(T, E, k);
-    if (lists && (!workspace || ws_bytes < need))
+    if (lists && need && (!workspace || ws_bytes < need))
         return fail(HFQ_ERR_WORKSPACE, "moe_route_scored: the lists need %zu bytes of workspace", need);
-    if (lists && !aligned16(workspace))
+    if (lists && need && !aligned16(workspace))
         return fail(HFQ_ERR_ALIGN, "moe_route_scored: the workspace must be 16-byte aligned");
 
     Args a;
     a.logits = logits; a.bias = bias; a.idx = idx; a.wts = wts;
-    a.hist = lists ? static_cast<int32_t *>(workspace) : nullptr;
+    a.hist = lists && need ? static_cast<uint16_t *>(workspace) : nullptr;
+    a.cnt = cnt; a.off = off; a.perm = perm;
     a.ld = ld ? ld : E; a.T = T; a.E = E; a.k = k;
     a.n_groups = n; a.size = E / n; a.topk_groups = rule->topk_groups; a.group_top = rule->group_top;
     a.tpl = pow2_floor(32 / n);
     a.run = (a.size + a.tpl - 1) / a.tpl;          // at most 30 (17 groups of 30)
+    a.tok = chunk_tokens(T);
     a.bf16 = logits_dtype == HFQ_BF16; a.sigmoid = rule->score == HFQ_SCORE_SIGMOID;
     a.renorm = rule->renormalise != 0; a.scale = rule->scale;
+    const int unit = a.bf16 ? 8 : 4;               // elements of 16 bytes
+    a.vec = aligned16(logits) && a.ld % unit == 0 && a.size % unit == 0 && a.run % unit == 0 && a.size % a.run == 0;
     cudaStream_t s = (cudaStream_t)stream;
-    const int chunks = (T + kTok - 1) / kTok;
-    if (a.run <= 8) route_scored_kernel<8><<<chunks, kWarps * 32, 0, s>>>(a);
-    else if (a.run <= 16) route_scored_kernel<16><<<chunks, kWarps * 32, 0, s>>>(a);
-    else route_scored_kernel<32><<<chunks, kWarps * 32, 0, s>>>(a);
-    if (lists) {
-        lists_scan_kernel<<<(E + 7) / 8, 256, 0, s>>>(a.hist, chunks, E, cnt);
-        lists_place_kernel<<<chunks, kListThr, 0, s>>>(idx, a.hist, cnt, T * k, kTok * k, E, off, perm);
+    if (!lists) {
+        // a warp a token up to one block an SM, then blocks of up to eight warps,
+        // which walk the tokens once there are more than eight blocks an SM
+        const int sms = std::max(1, sm_count());
+        const int warps = T <= sms ? 1 : T <= 4 * sms ? 4 : 8;
+        const int grid = std::min((T + warps - 1) / warps, 8 * sms);
+        if (a.run <= 8) route_scored_kernel<8><<<grid, warps * 32, 0, s>>>(a);
+        else if (a.run <= 16) route_scored_kernel<16><<<grid, warps * 32, 0, s>>>(a);
+        else route_scored_kernel<32><<<grid, warps * 32, 0, s>>>(a);
+    } else {
+        const int chunks = (T + a.tok - 1) / a.tok, thr = kListWarps * 32;
+        if (a.run <= 8) route_count_kernel<8><<<chunks, thr, 0, s>>>(a);
+        else if (a.run <= 16) route_count_kernel<16><<<chunks, thr, 0, s>>>(a);
+        else route_count_kernel<32><<<chunks, thr, 0, s>>>(a);
+        if (need) {
+            int32_t *base = nullptr;
+            int group = (chunks + 73) / 74;
+            if (chunks > kScanChunks) {
+                base = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + round256((size_t)chunks * E * 2));
+                lists_scan_kernel<<<(E + 7) / 8, 256, 0, s>>>(a.hist, chunks, E, base, cnt);
+                group = 1;
+            }
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((chunks + group - 1) / group);
+            cfg.blockDim = dim3(thr);
+            cfg.stream = s;
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr.val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = base ? 0 : 1;           // behind the counting kernel it may start early
+            const cudaError_t e = cudaLaunchKernelEx(&cfg, lists_place_kernel, (const int32_t *)idx,
+                                                     (const uint16_t *)a.hist, (const int32_t *)base, chunks, group,
+                                                     T * k, a.tok * k, E, cnt, off, perm);
+            if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "moe_route_scored launch: %s", cudaGetErrorString(e));
+        }
     }
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return fail(HFQ_ERR_CUDA, "moe_route_scored launch: %s", cudaGetErrorString(err));

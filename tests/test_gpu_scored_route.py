@@ -215,3 +215,37 @@ def test_captured_and_replayed_with_a_shared_workspace(eo):
             np.testing.assert_array_equal(o[0].view(-1, k).cpu().numpy(), idx)
             for t, v in zip(o[2:], route.group_by_expert(idx, E)):
                 np.testing.assert_array_equal(t.cpu().numpy(), v)
+
+
+@pytest.mark.parametrize("T", [1, 16, 17, 70])
+@pytest.mark.parametrize("score", [0, 1], ids=["softmax", "sigmoid"])
+def test_groups_closer_than_32_bits_tell_apart(eo, T, score):
+    """Sums of a group's two best that differ by less than an f32 step, through
+    the bias; ordinary members below them."""
+    rng = np.random.default_rng(T + score)
+    E, n = 256, 8
+    l = rng.standard_normal((1, E)).astype(np.float32).repeat(T, 0)
+    x = l[0].astype(np.float64)
+    p = 1 / (1 + np.exp(-x)) if score else np.exp(x - x.max()) / np.exp(x - x.max()).sum()
+    bias = np.zeros(E, np.float32)
+    for g in range(n):                                   # two members each near 2, the sum within f32 rounding of 4
+        for j, target in ((3, 2.0), (9, 2.0)):
+            bias[g * 32 + j] = np.float32(target - p[g * 32 + j])
+    _check(eo, torch.from_numpy(l).cuda(), 8, dict(score=score, n_groups=n, topk_groups=4, group_top=2),
+           bias=torch.from_numpy(bias).cuda(), lists=True)
+    _check(eo, torch.from_numpy(l).cuda(), 3, dict(score=score, n_groups=n, topk_groups=2, group_top=1),
+           bias=torch.from_numpy(bias).cuda(), lists=True)
+
+
+@pytest.mark.parametrize("T,E,k", [(5000, 300, 5), (9000, 512, 8), (16384, 64, 2), (16385, 33, 4), (65536, 16, 1)])
+def test_lists_of_every_chunk_size(eo, T, E, k):
+    """Chunks of 16, 32 and 64 tokens, counts added up by the placing blocks and by a kernel between."""
+    l = _rand(T, E, T + 1, std=2.0)
+    got = _run(eo, l, k, dict(score=0), lists=True)
+    idx = torch.sort(l, dim=1, descending=True, stable=True).indices[:, :k].int().cpu().numpy()
+    np.testing.assert_array_equal(got[0], idx)
+    flat = idx.reshape(-1).astype(np.int64)
+    cnt = np.bincount(flat, minlength=E)
+    np.testing.assert_array_equal(got[2], cnt)
+    np.testing.assert_array_equal(got[3], np.concatenate([[0], np.cumsum(cnt)]))
+    np.testing.assert_array_equal(got[4], np.argsort(flat, kind="stable"))
