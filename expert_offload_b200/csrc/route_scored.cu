@@ -29,8 +29,9 @@ namespace hfq {
 namespace {
 
 constexpr int kMaxCand = 32;     // candidates: one a lane
-constexpr int kListWarps = 16;   // warps of a block with lists
-constexpr int kTokMax = 64;      // tokens of a block with lists, at most: one chunk of the pair lists
+constexpr int kListWarps = 8;    // warps of a block that counts for the lists
+constexpr int kTokMax = 32;      // tokens of such a block, at most: one chunk of the pair lists
+constexpr int kAlone = 16;       // tokens that one block takes with their lists
 constexpr int kScanChunks = 256; // chunks that the placing blocks add up by themselves
 
 struct Args {
@@ -188,14 +189,16 @@ __device__ __noinline__ Slot select64(const Args &a, size_t row, int lane, float
     return slot;
 }
 
-// Largest of the lanes' values (redux of an order-preserving map; -inf is below
-// all others, NaN does not occur).
-__device__ __forceinline__ float redux_max(float v)
+// Order-preserving map of a float (not NaN) to a word above 0, and back.
+__device__ __forceinline__ uint32_t order32(float v)
 {
-    const uint32_t b = __float_as_uint(v + 0.0f);
-    const uint32_t m = __reduce_max_sync(0xffffffffu, b >> 31 ? ~b : b | 0x80000000u);
-    return __uint_as_float(m >> 31 ? m & 0x7fffffffu : ~m);
+    const uint32_t b = __float_as_uint(v + 0.0f);        // -0 and +0 are equal
+    return b >> 31 ? ~b : b | 0x80000000u;
 }
+
+__device__ __forceinline__ float value32(uint32_t m) { return __uint_as_float(m >> 31 ? m & 0x7fffffffu : ~m); }
+
+__device__ __forceinline__ float redux_max(float v) { return value32(__reduce_max_sync(0xffffffffu, order32(v))); }
 
 // Selection score of expert e in 64 bits, from its logit.
 __device__ __forceinline__ double score64(const Args &a, float l, int e, float m, double inv_z)
@@ -208,7 +211,15 @@ __device__ __forceinline__ double score64(const Args &a, float l, int e, float m
 __device__ __forceinline__ float rcp_approx(float v)
 {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// exp(v) from the exponential's unit: results below 2^-126 are 0.
+__device__ __forceinline__ float exp_approx(float v)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v * 1.4426950408889634f));
     return r;
 }
 
@@ -226,7 +237,7 @@ __device__ __noinline__ double inv_sum64(const Args &a, size_t row, int lane, fl
 // Selection score of expert e in f32 (see select_token for its error).
 __device__ __forceinline__ float score32(const Args &a, float l, float b, float m, float inv_z)
 {
-    const float s = a.sigmoid ? rcp_approx(1.0f + __expf(-l)) : __expf(l - m) * inv_z;
+    const float s = a.sigmoid ? rcp_approx(1.0f + exp_approx(-l)) : exp_approx(l - m) * inv_z;
     return l > -INFINITY ? s + b : -INFINITY;
 }
 
@@ -368,31 +379,42 @@ __device__ __forceinline__ Slot select_token(const Args &a, size_t row, const fl
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < N; ++i) top = fmaxf(top, c[i]);
-    if (!keep) top = -INFINITY;
-    float best = 0.0f, bound = -INFINITY;
+    uint32_t mine = keep ? order32(top) : 0u, first = 0, last = 0;
     for (int j = 0; j < a.k; ++j) {
-        bound = redux_max(top);
-        if (j == 0) best = bound;
-        if (!(bound > -INFINITY)) break;
-        if (top == bound) top = -INFINITY;
+        last = __reduce_max_sync(0xffffffffu, mine);
+        if (j == 0) first = last;
+        mine = mine == last ? 0u : mine;
     }
-    const float margin = a.bias ? 2.0f * (base + kU * fmaxf(fabsf(best), bound > -INFINITY ? fabsf(bound) : 0.0f)) : 0.0f;
-    const float low = bound - 2.0f * margin;
-    int n = 0;
+    // 0: fewer distinct maxima than k; every live expert is a candidate then
+    const float best = first ? value32(first) : -INFINITY, bound = last ? value32(last) : -INFINITY;
+    const float low = fmaxf(a.bias ? bound - 4.0f * (base + kU * fmaxf(fabsf(best), fabsf(bound))) : bound, -FLT_MAX);
+    uint32_t in = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const bool in = keep && c[i] > -INFINITY && c[i] >= low;
-        const unsigned who = __ballot_sync(0xffffffffu, in);
+    for (int i = 0; i < N; ++i) in |= (c[i] >= low ? 1u : 0u) << i;
+    if (!keep) in = 0;
+    int n = 0;
+    for (unsigned who; (who = __ballot_sync(0xffffffffu, in != 0)) != 0;) {
         const int at = n + __popc(who & ((1u << lane) - 1u));
-        if (in && at < kMaxCand) cand.c[at] = c[i], cand.l[at] = l[i], cand.e[at] = e0 + i;
+        if (in && at < kMaxCand) cand.e[at] = e0 + __ffs(in) - 1;
+        in &= in - 1;
         n += __popc(who);
     }
     if (n < a.k || n > kMaxCand) {
         return select64<N>(a, row, lane, m);
     }
     __syncwarp();
-    const float mc = lane < n ? cand.c[lane] : -INFINITY, ml = lane < n ? cand.l[lane] : -INFINITY;
-    const int me = lane < n ? cand.e[lane] : 0x7fffffff;
+    // each lane its candidate, from its logit once more (the same bits)
+    float mc = -INFINITY, ml = -INFINITY;
+    int me = 0x7fffffff;
+    if (lane < n) {
+        me = cand.e[lane];
+        ml = read_logit(a, row, me);
+        mc = a.bias ? score32(a, ml, a.bias[me], m, a.sigmoid ? 1.0f : smax) : ml;
+        cand.c[lane] = mc;
+    }
+    __syncwarp();
+    const float big = a.bias ? __uint_as_float(__reduce_max_sync(0xffffffffu, lane < n ? __float_as_uint(fabsf(mc)) : 0u)) : 0.0f;
+    const float margin = a.bias ? 2.0f * (base + kU * big) : 0.0f;
     int rank = 0;
     bool close = false;
     for (int j = 0; j < n; ++j) {
@@ -419,22 +441,30 @@ __device__ __forceinline__ Slot select_token(const Args &a, size_t row, const fl
     return slot;
 }
 
-// The lane's logits (masked ones -inf) and biases.
+// The lane's biases; `masks`: some expert of the token's has one that masks it.
 template <int N>
-__device__ __forceinline__ void read_bias(const Args &a, int e0, int n, float (&b)[N])
+__device__ __forceinline__ void read_bias(const Args &a, int e0, int n, float (&b)[N], bool &masks)
 {
+    bool odd = false;
 #pragma unroll
-    for (int i = 0; i < N; ++i) b[i] = a.bias && i < n ? a.bias[e0 + i] : 0.0f;
+    for (int i = 0; i < N; ++i) {
+        b[i] = a.bias && i < n ? a.bias[e0 + i] : 0.0f;
+        odd |= !(b[i] > -INFINITY);
+    }
+    masks = __any_sync(0xffffffffu, odd);
 }
 
+// The lane's logits, masked ones -inf.
+
 template <int N>
-__device__ __forceinline__ void read_logits(const Args &a, size_t row, int e0, int n, const float (&b)[N], float (&l)[N])
+__device__ __forceinline__ void read_logits(const Args &a, size_t row, int e0, int n, const float (&b)[N], bool masks,
+                                            float (&l)[N])
 {
     if (a.vec) {                 // whole 16-byte pieces
         if (a.bf16) {
 #pragma unroll
             for (int i = 0; i < N; i += 8) {
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                uint4 v = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);    // -inf
                 if (i < n) v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.logits) + row + e0 + i);
                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -444,7 +474,7 @@ __device__ __forceinline__ void read_logits(const Args &a, size_t row, int e0, i
         } else {
 #pragma unroll
             for (int i = 0; i < N; i += 4) {
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
                 if (i < n) v = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + row + e0 + i);
                 l[i] = v.x, l[i + 1] = v.y, l[i + 2] = v.z, l[i + 3] = v.w;
             }
@@ -452,26 +482,31 @@ __device__ __forceinline__ void read_logits(const Args &a, size_t row, int e0, i
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
-            l[i] = i >= n    ? 0.0f
+            l[i] = i >= n    ? -INFINITY
                    : a.bf16  ? bf16_bits_to_float(static_cast<const uint16_t *>(a.logits)[row + e0 + i])
                              : static_cast<const float *>(a.logits)[row + e0 + i];
     }
+    const float least = n > 0 ? -FLT_MAX : INFINITY;     // a lane without experts has none
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        l[i] = i < n && l[i] > -INFINITY && b[i] > -INFINITY ? fminf(l[i], FLT_MAX) : -INFINITY;
+    for (int i = 0; i < N; ++i) l[i] = l[i] >= least ? fminf(l[i], FLT_MAX) : -INFINITY;
+    if (masks) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (!(b[i] > -INFINITY)) l[i] = -INFINITY;
+    }
 }
 
 // The whole of one token; lane j < k ends with its slot j.
 template <int N>
-__device__ __forceinline__ void route_token(const Args &a, int t, int lane, const float (&b)[N], Cand &cand, int &e,
-                                            float &w)
+__device__ __forceinline__ void route_token(const Args &a, int t, int lane, const float (&b)[N], bool masks,
+                                            Cand &cand, int &e, float &w)
 {
     const int grp = lane / a.tpl, part = lane - grp * a.tpl;
     const int e0 = grp * a.size + part * a.run;
     const int n = grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0;
     const size_t row = (size_t)t * a.ld;
     float l[N];
-    read_logits(a, row, e0, n, b, l);
+    read_logits(a, row, e0, n, b, masks, l);
     float m = 0.0f, z = 1.0f;
     if (!a.sigmoid && (a.bias || !a.renorm || a.group_top > 1)) {
         m = -INFINITY;
@@ -481,7 +516,7 @@ __device__ __forceinline__ void route_token(const Args &a, int t, int lane, cons
         if (!(m > -INFINITY)) m = 0.0f;
         z = 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) z += __expf(l[i] - m);
+        for (int i = 0; i < N; ++i) z += exp_approx(l[i] - m);
         z = warp_sum(z);
     }
     const Slot slot = select_token<N>(a, row, l, b, lane, m, z, cand);
@@ -502,45 +537,56 @@ __global__ void __launch_bounds__(256) route_scored_kernel(const Args a)
     const int grp = lane / a.tpl, part = lane - grp * a.tpl;
     float b[N], w;
     int e;
-    read_bias(a, grp * a.size + part * a.run, grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0, b);
-    for (int t = blockIdx.x * warps + warp; t < a.T; t += gridDim.x * warps) route_token<N>(a, t, lane, b, cand[warp], e, w);
+    bool masks;
+    read_bias(a, grp * a.size + part * a.run, grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0, b, masks);
+    for (int t = blockIdx.x * warps + warp; t < a.T; t += gridDim.x * warps) route_token<N>(a, t, lane, b, masks, cand[warp], e, w);
 }
 
 // ------------------------------------------------------------ the pair lists
 // Pairs are placed in order: `start[e]` is where expert e's next pair goes.
-// `p0` .. `p1` are handled, all threads of the block together, and start moves on.
+// Up to 512 at a time: a warp ranks its 32 among themselves, a table of the
+// warps' counts puts them behind the warps before.
+constexpr int kPlaceWarps = 16, kPlaceThr = kPlaceWarps * 32;
+
 struct Placer {
     int start[HFQ_MAX_EXPERTS];
-    unsigned short wcnt[kListWarps][HFQ_MAX_EXPERTS];    // zero between passes
+    unsigned short wcnt[kPlaceWarps][HFQ_MAX_EXPERTS];
 };
 
-__device__ __forceinline__ void place_pairs(Placer &s, const int32_t *idx, int p0, int p1, int E, int32_t *perm)
+__device__ __forceinline__ void clear_counts(Placer &s)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int q = p0; q < p1; q += kListWarps * 32) {
-        const int p = q + tid;
-        const int e = p < p1 ? idx[p] : -1;
-        const unsigned same = __match_any_sync(0xffffffffu, e);
-        const int rank = __popc(same & ((1u << lane) - 1u));
-        if (e >= 0 && rank == 0) s.wcnt[warp][e] = (unsigned short)__popc(same);
-        __syncthreads();
-        if (e >= 0) {
-            int pos = s.start[e] + rank;
-            for (int w = 0; w < warp; ++w) pos += s.wcnt[w][e];
-            perm[pos] = p;
-        }
-        __syncthreads();
-        for (int x = tid; x < E; x += kListWarps * 32) {
-            int n = 0;
-#pragma unroll
-            for (int w = 0; w < kListWarps; ++w) {
-                n += s.wcnt[w][x];
-                s.wcnt[w][x] = 0;
-            }
-            s.start[x] += n;
-        }
-        __syncthreads();
+    uint4 *p = reinterpret_cast<uint4 *>(s.wcnt);
+    for (int i = threadIdx.x; i < (int)sizeof(s.wcnt) / 16; i += kPlaceThr) p[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// `e` = the expert of this thread's pair p (-1: none); the counts are zero.
+__device__ __forceinline__ void place_pairs(Placer &s, int e, int p, int32_t *perm)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned same = __match_any_sync(0xffffffffu, e);
+    const int rank = __popc(same & ((1u << lane) - 1u));
+    if (e >= 0 && rank == 0) s.wcnt[warp][e] = (unsigned short)__popc(same);
+    __syncthreads();
+    if (e >= 0) {
+        int pos = s.start[e] + rank;
+        for (int w = 0; w < warp; ++w) pos += s.wcnt[w][e];
+        perm[pos] = p;
     }
+}
+
+// Moves the starts behind the pairs just placed and clears their counts.
+__device__ __forceinline__ void next_pairs(Placer &s, int E)
+{
+    __syncthreads();
+    for (int x = threadIdx.x; x < E; x += kPlaceThr) {
+        int n = 0;
+        for (int w = 0; w < kPlaceWarps; ++w) {
+            n += s.wcnt[w][x];
+            s.wcnt[w][x] = 0;
+        }
+        s.start[x] += n;
+    }
+    __syncthreads();
 }
 
 // Exclusive sums of the totals of all experts (thread e holds expert e's).
@@ -560,44 +606,63 @@ __device__ __forceinline__ int exclusive_sum(int v, int *wsum)
     return before + s - v;
 }
 
-// With lists: a block routes a.tok tokens and counts its pairs; a block that has
-// all tokens writes the lists, too.
+// With lists, several chunks: a block routes a.tok tokens and counts its pairs.
 template <int N>
 __global__ void __launch_bounds__(kListWarps * 32) route_count_kernel(const Args a)
 {
-    __shared__ union {
-        Cand cand[kListWarps];
-        Placer place;
-    } s;
-    __shared__ int count[HFQ_MAX_EXPERTS], wsum[kListWarps];
+    __shared__ Cand cand[kListWarps];
+    __shared__ int count[HFQ_MAX_EXPERTS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int grp = lane / a.tpl, part = lane - grp * a.tpl;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    count[tid] = 0;
+    for (int i = tid; i < a.E; i += kListWarps * 32) count[i] = 0;
     float b[N], w;
     int e;
-    read_bias(a, grp * a.size + part * a.run, grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0, b);
+    bool masks;
+    read_bias(a, grp * a.size + part * a.run, grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0, b, masks);
     __syncthreads();
     const int t_end = min(a.T, ((int)blockIdx.x + 1) * a.tok);
     for (int t = blockIdx.x * a.tok + warp; t < t_end; t += kListWarps) {
-        route_token<N>(a, t, lane, b, s.cand[warp], e, w);
+        route_token<N>(a, t, lane, b, masks, cand[warp], e, w);
         if (lane < a.k) atomicAdd(&count[e], 1);
     }
     __syncthreads();
-    if (a.hist) {
-        if (tid < a.E) a.hist[(size_t)blockIdx.x * a.E + tid] = (uint16_t)count[tid];
-        return;
-    }
-    const int mine = exclusive_sum(count[tid], wsum);
-    s.place.start[tid] = mine;
-    for (int w2 = 0; w2 < kListWarps; ++w2) s.place.wcnt[w2][tid] = 0;
-    if (tid < a.E) {
-        a.cnt[tid] = count[tid];
-        a.off[tid] = mine;
-        if (tid == a.E - 1) a.off[a.E] = mine + count[tid];
+    for (int i = tid; i < a.E; i += kListWarps * 32) a.hist[(size_t)blockIdx.x * a.E + i] = (uint16_t)count[i];
+}
+
+// With lists, up to 16 tokens: one block routes them, a warp each, and writes
+// the lists.
+template <int N>
+__global__ void __launch_bounds__(kPlaceThr) route_alone_kernel(const Args a)
+{
+    __shared__ Cand cand[kPlaceWarps];
+    __shared__ __align__(16) Placer place;
+    __shared__ int wsum[kPlaceWarps], sel[kPlaceWarps * HFQ_MAX_TOPK];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int grp = lane / a.tpl, part = lane - grp * a.tpl;
+    float b[N], w;
+    int e;
+    bool masks;
+    read_bias(a, grp * a.size + part * a.run, grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0, b, masks);
+    clear_counts(place);
+    place.start[tid] = 0;
+    __syncthreads();
+    if (warp < a.T) {
+        route_token<N>(a, warp, lane, b, masks, cand[warp], e, w);
+        if (lane < a.k) {
+            sel[warp * a.k + lane] = e;
+            atomicAdd(&place.start[e], 1);
+        }
     }
     __syncthreads();
-    place_pairs(s.place, a.idx, 0, a.T * a.k, a.E, a.perm);      // idx: written by this block
+    const int total = place.start[tid], sum = exclusive_sum(total, wsum);
+    place.start[tid] = sum;
+    if (tid < a.E) {
+        a.cnt[tid] = total;
+        a.off[tid] = sum;
+        if (tid == a.E - 1) a.off[a.E] = sum + total;
+    }
+    place_pairs(place, tid < a.T * a.k ? sel[tid] : -1, tid, a.perm);     // its barrier covers start, too
 }
 
 // Adds up the counts of many chunks, expert by expert, a warp each: base[c][e]
@@ -626,45 +691,65 @@ __global__ void lists_scan_kernel(const uint16_t *__restrict__ hist, int chunks,
 // Places the pairs of `group` consecutive chunks.  The counts of the chunks
 // before come from base, or (base null) are added up here: all blocks read all
 // counts, 256 x 512 x 2 bytes at most, instead of a kernel between.
-__global__ void __launch_bounds__(kListWarps * 32)
+__global__ void __launch_bounds__(kPlaceThr)
 lists_place_kernel(const int32_t *__restrict__ idx, const uint16_t *__restrict__ hist, const int32_t *__restrict__ base,
                    int chunks, int group, int P, int per_chunk, int E, int32_t *__restrict__ cnt,
                    int32_t *__restrict__ off, int32_t *__restrict__ perm)
 {
-    __shared__ Placer s;
-    __shared__ int wsum[kListWarps];
+    __shared__ __align__(16) Placer s;
+    __shared__ int wsum[kPlaceWarps], total_of[HFQ_MAX_EXPERTS], before_of[HFQ_MAX_EXPERTS];
     const int tid = threadIdx.x;
     const int first = blockIdx.x * group;
-    for (int w = 0; w < kListWarps; ++w) s.wcnt[w][tid] = 0;
+    total_of[tid] = before_of[tid] = 0;
+    clear_counts(s);
+    __syncthreads();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    int before = 0, total = 0;
-    if (tid < E) {
-        if (base) {
-            before = base[(size_t)first * E + tid];
-            total = cnt[tid];
-        } else {
-            constexpr int kU = 16;
-            for (int c0 = 0; c0 < chunks; c0 += kU) {
-                int v[kU];
+    if (base) {
+        if (tid < E) before_of[tid] = base[(size_t)first * E + tid], total_of[tid] = cnt[tid];
+    } else {
+        // a thread adds two neighbours' counts in every kRows-th chunk, many in flight
+        const int half = (E + 1) / 2, lanes = half <= 64 ? 64 : half <= 128 ? 128 : 256, rows = kPlaceThr / lanes;
+        const int x = (tid & (lanes - 1)) * 2, r0 = tid / lanes;
+        int t0 = 0, t1 = 0, b0 = 0, b1 = 0;
+        constexpr int kU = 16;
+        if (x < E) {
+            for (int c0 = r0; c0 < chunks; c0 += kU * rows) {
+                int u[kU], v[kU];
 #pragma unroll
-                for (int u = 0; u < kU; ++u) v[u] = c0 + u < chunks ? hist[(size_t)(c0 + u) * E + tid] : 0;
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    total += v[u];
-                    if (c0 + u < first) before += v[u];
+                for (int i = 0; i < kU; ++i) {
+                    const int c = c0 + i * rows;
+                    const uint16_t *h = hist + (size_t)c * E + x;
+                    u[i] = c < chunks ? h[0] : 0;
+                    v[i] = c < chunks && x + 1 < E ? h[1] : 0;
                 }
+#pragma unroll
+                for (int i = 0; i < kU; ++i) {
+                    t0 += u[i], t1 += v[i];
+                    if (c0 + i * rows < first) b0 += u[i], b1 += v[i];
+                }
+            }
+            atomicAdd(&total_of[x], t0);
+            atomicAdd(&before_of[x], b0);
+            if (x + 1 < E) {
+                atomicAdd(&total_of[x + 1], t1);
+                atomicAdd(&before_of[x + 1], b1);
             }
         }
     }
-    const int sum = exclusive_sum(total, wsum);
-    s.start[tid] = sum + before;
+    __syncthreads();
+    const int total = total_of[tid], sum = exclusive_sum(total, wsum);
+    s.start[tid] = sum + before_of[tid];
     if (blockIdx.x == 0 && tid < E) {
         off[tid] = sum;
         if (!base) cnt[tid] = total;
         if (tid == E - 1) off[E] = sum + total;
     }
-    __syncthreads();
-    place_pairs(s, idx, first * per_chunk, min(P, (first + group) * per_chunk), E, perm);
+    const int p1 = min(P, (first + group) * per_chunk);
+    for (int p0 = first * per_chunk; p0 < p1; p0 += kPlaceThr) {
+        const int p = p0 + tid;
+        if (p0 > first * per_chunk) next_pairs(s, E);
+        place_pairs(s, p < p1 ? idx[p] : -1, p, perm);
+    }
 }
 
 // Tokens of a chunk: one for each warp of its block until the chunks fill the
@@ -692,7 +777,7 @@ extern "C" {
 // tokens.
 size_t moe_route_scored_workspace_bytes(int T, int E, int k)
 {
-    if (T < 1 || E < 1 || k < 1 || T <= kListWarps) return 0;
+    if (T < 1 || E < 1 || k < 1 || T <= kAlone) return 0;
     const size_t chunks = ((size_t)T + chunk_tokens(T) - 1) / chunk_tokens(T);
     return round256(chunks * E * sizeof(uint16_t)) + (chunks > kScanChunks ? chunks * E * sizeof(int32_t) : 0);
 }
@@ -762,20 +847,23 @@ hfq_status moe_route_scored(const void *logits, hfq_dtype logits_dtype, int ld, 
         else route_scored_kernel<32><<<grid, warps * 32, 0, s>>>(a);
     } else {
         const int chunks = (T + a.tok - 1) / a.tok, thr = kListWarps * 32;
-        if (a.run <= 8) route_count_kernel<8><<<chunks, thr, 0, s>>>(a);
-        else if (a.run <= 16) route_count_kernel<16><<<chunks, thr, 0, s>>>(a);
-        else route_count_kernel<32><<<chunks, thr, 0, s>>>(a);
-        if (need) {
+        if (!need) {
+            if (a.run <= 8) route_alone_kernel<8><<<1, kPlaceThr, 0, s>>>(a);
+            else if (a.run <= 16) route_alone_kernel<16><<<1, kPlaceThr, 0, s>>>(a);
+            else route_alone_kernel<32><<<1, kPlaceThr, 0, s>>>(a);
+        } else {
+            if (a.run <= 8) route_count_kernel<8><<<chunks, thr, 0, s>>>(a);
+            else if (a.run <= 16) route_count_kernel<16><<<chunks, thr, 0, s>>>(a);
+            else route_count_kernel<32><<<chunks, thr, 0, s>>>(a);
             int32_t *base = nullptr;
-            int group = (chunks + 73) / 74;
+            int group = std::max(1, kPlaceThr / (a.tok * k));       // one pass of a placing block
             if (chunks > kScanChunks) {
                 base = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + round256((size_t)chunks * E * 2));
                 lists_scan_kernel<<<(E + 7) / 8, 256, 0, s>>>(a.hist, chunks, E, base, cnt);
-                group = 1;
             }
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3((chunks + group - 1) / group);
-            cfg.blockDim = dim3(thr);
+            cfg.blockDim = dim3(kPlaceThr);
             cfg.stream = s;
             cudaLaunchAttribute attr;
             attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
