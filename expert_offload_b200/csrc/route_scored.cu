@@ -47,7 +47,7 @@ struct Args {
     int tpl, run;                // lanes of a group, experts of a lane
     int tok;                     // tokens of a block (lists)
     int bf16, sigmoid, renorm;
-    int vec;                     // runs are whole 16-byte pieces of the logits
+    int vec, bias_vec;           // runs are whole 16-byte pieces of the logits, of the bias
     float scale;
 };
 
@@ -100,7 +100,7 @@ __device__ __forceinline__ float weight_of(const Args &a, float l, int lane, flo
     float s = live ? expf(e - top) : 0.0f;
     if (a.sigmoid && live) s /= 1.0f + expf(-fabsf(l));
     const float sum = warp_sum(s);
-    return sum > 0.0f ? s / sum * a.scale : 0.0f;
+    return sum > 0.0f ? s * (a.scale / sum) : 0.0f;
 }
 
 struct Slot {
@@ -235,10 +235,16 @@ __device__ __noinline__ double inv_sum64(const Args &a, size_t row, int lane, fl
 }
 
 // Selection score of expert e in f32 (see select_token for its error).
+template <bool SIGMOID>
+__device__ __forceinline__ float score32(float l, float b, float m, float inv_z)
+{
+    const float s = SIGMOID ? rcp_approx(1.0f + exp_approx(-l)) : exp_approx(l - m) * inv_z;
+    return l > -INFINITY ? s + b : -INFINITY;
+}
+
 __device__ __forceinline__ float score32(const Args &a, float l, float b, float m, float inv_z)
 {
-    const float s = a.sigmoid ? rcp_approx(1.0f + exp_approx(-l)) : exp_approx(l - m) * inv_z;
-    return l > -INFINITY ? s + b : -INFINITY;
+    return a.sigmoid ? score32<true>(l, b, m, inv_z) : score32<false>(l, b, m, inv_z);
 }
 
 struct Cand {                    // of a warp
@@ -318,11 +324,15 @@ __device__ __forceinline__ Slot select_token(const Args &a, size_t row, const fl
     if (scored) {
         float s[N];
         const float zi = a.sigmoid ? 1.0f : smax;
+        if (a.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            s[i] = score32(a, l[i], b[i], m, zi);
-            c[i] = a.bias ? s[i] : l[i];
+            for (int i = 0; i < N; ++i) s[i] = score32<true>(l[i], b[i], m, zi);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) s[i] = score32<false>(l[i], b[i], m, zi);
         }
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = a.bias ? s[i] : l[i];
         if (a.n_groups > 1) {
             float t1 = -INFINITY, t2 = -INFINITY;
 #pragma unroll
@@ -441,17 +451,30 @@ __device__ __forceinline__ Slot select_token(const Args &a, size_t row, const fl
     return slot;
 }
 
-// The lane's biases; `masks`: some expert of the token's has one that masks it.
-template <int N>
-__device__ __forceinline__ void read_bias(const Args &a, int e0, int n, float (&b)[N], bool &masks)
+// Whether some expert has a bias that masks it.
+__device__ __forceinline__ bool bias_masks(const Args &a, int lane)
 {
     bool odd = false;
+    if (a.bias)
+        for (int e = lane; e < a.E; e += 32) odd |= !(a.bias[e] > -INFINITY);
+    return __any_sync(0xffffffffu, odd);
+}
+
+// The lane's biases, from L1 for all but an SM's first tokens.
+template <int N>
+__device__ __forceinline__ void read_bias(const Args &a, int e0, int n, float (&b)[N])
+{
+    if (a.bias && a.bias_vec) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        b[i] = a.bias && i < n ? a.bias[e0 + i] : 0.0f;
-        odd |= !(b[i] > -INFINITY);
+        for (int i = 0; i < N; i += 4) {
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i < n) v = __ldg(reinterpret_cast<const float4 *>(a.bias + e0 + i));
+            b[i] = v.x, b[i + 1] = v.y, b[i + 2] = v.z, b[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) b[i] = a.bias && i < n ? __ldg(a.bias + e0 + i) : 0.0f;
     }
-    masks = __any_sync(0xffffffffu, odd);
 }
 
 // The lane's logits, masked ones -inf.
@@ -498,14 +521,15 @@ __device__ __forceinline__ void read_logits(const Args &a, size_t row, int e0, i
 
 // The whole of one token; lane j < k ends with its slot j.
 template <int N>
-__device__ __forceinline__ void route_token(const Args &a, int t, int lane, const float (&b)[N], bool masks,
-                                            Cand &cand, int &e, float &w)
+__device__ __forceinline__ void route_token(const Args &a, int t, int lane, bool masks, Cand &cand, int &e,
+                                            float &w)
 {
     const int grp = lane / a.tpl, part = lane - grp * a.tpl;
     const int e0 = grp * a.size + part * a.run;
     const int n = grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0;
     const size_t row = (size_t)t * a.ld;
-    float l[N];
+    float l[N], b[N];
+    read_bias(a, e0, n, b);
     read_logits(a, row, e0, n, b, masks, l);
     float m = 0.0f, z = 1.0f;
     if (!a.sigmoid && (a.bias || !a.renorm || a.group_top > 1)) {
@@ -530,16 +554,14 @@ __device__ __forceinline__ void route_token(const Args &a, int t, int lane, cons
 
 // Without lists: warps walk the tokens.
 template <int N>
-__global__ void __launch_bounds__(256) route_scored_kernel(const Args a)
+__global__ void __launch_bounds__(256, N > 16 ? 1 : 3) route_scored_kernel(const Args a)
 {
     __shared__ Cand cand[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int grp = lane / a.tpl, part = lane - grp * a.tpl;
-    float b[N], w;
+    float w;
     int e;
-    bool masks;
-    read_bias(a, grp * a.size + part * a.run, grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0, b, masks);
-    for (int t = blockIdx.x * warps + warp; t < a.T; t += gridDim.x * warps) route_token<N>(a, t, lane, b, masks, cand[warp], e, w);
+    const bool masks = bias_masks(a, lane);
+    for (int t = blockIdx.x * warps + warp; t < a.T; t += gridDim.x * warps) route_token<N>(a, t, lane, masks, cand[warp], e, w);
 }
 
 // ------------------------------------------------------------ the pair lists
@@ -608,22 +630,20 @@ __device__ __forceinline__ int exclusive_sum(int v, int *wsum)
 
 // With lists, several chunks: a block routes a.tok tokens and counts its pairs.
 template <int N>
-__global__ void __launch_bounds__(kListWarps * 32) route_count_kernel(const Args a)
+__global__ void __launch_bounds__(kListWarps * 32, N > 16 ? 1 : 4) route_count_kernel(const Args a)
 {
     __shared__ Cand cand[kListWarps];
     __shared__ int count[HFQ_MAX_EXPERTS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int grp = lane / a.tpl, part = lane - grp * a.tpl;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     for (int i = tid; i < a.E; i += kListWarps * 32) count[i] = 0;
-    float b[N], w;
+    float w;
     int e;
-    bool masks;
-    read_bias(a, grp * a.size + part * a.run, grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0, b, masks);
+    const bool masks = bias_masks(a, lane);
     __syncthreads();
     const int t_end = min(a.T, ((int)blockIdx.x + 1) * a.tok);
     for (int t = blockIdx.x * a.tok + warp; t < t_end; t += kListWarps) {
-        route_token<N>(a, t, lane, b, masks, cand[warp], e, w);
+        route_token<N>(a, t, lane, masks, cand[warp], e, w);
         if (lane < a.k) atomicAdd(&count[e], 1);
     }
     __syncthreads();
@@ -639,16 +659,14 @@ __global__ void __launch_bounds__(kPlaceThr) route_alone_kernel(const Args a)
     __shared__ __align__(16) Placer place;
     __shared__ int wsum[kPlaceWarps], sel[kPlaceWarps * HFQ_MAX_TOPK];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int grp = lane / a.tpl, part = lane - grp * a.tpl;
-    float b[N], w;
+    float w;
     int e;
-    bool masks;
-    read_bias(a, grp * a.size + part * a.run, grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0, b, masks);
+    const bool masks = bias_masks(a, lane);
     clear_counts(place);
     place.start[tid] = 0;
     __syncthreads();
     if (warp < a.T) {
-        route_token<N>(a, warp, lane, b, masks, cand[warp], e, w);
+        route_token<N>(a, warp, lane, masks, cand[warp], e, w);
         if (lane < a.k) {
             sel[warp * a.k + lane] = e;
             atomicAdd(&place.start[e], 1);
@@ -691,8 +709,9 @@ __global__ void lists_scan_kernel(const uint16_t *__restrict__ hist, int chunks,
 // Places the pairs of `group` consecutive chunks.  The counts of the chunks
 // before come from base, or (base null) are added up here: all blocks read all
 // counts, 256 x 512 x 2 bytes at most, instead of a kernel between.
+static_assert(kScanChunks * kTokMax < 65536, "sums of the counts fit 16 bits");
 __global__ void __launch_bounds__(kPlaceThr)
-lists_place_kernel(const int32_t *__restrict__ idx, const uint16_t *__restrict__ hist, const int32_t *__restrict__ base,
+lists_place_kernel(const int32_t *idx, const uint16_t *hist, const int32_t *__restrict__ base,
                    int chunks, int group, int P, int per_chunk, int E, int32_t *__restrict__ cnt,
                    int32_t *__restrict__ off, int32_t *__restrict__ perm)
 {
@@ -707,33 +726,50 @@ lists_place_kernel(const int32_t *__restrict__ idx, const uint16_t *__restrict__
     if (base) {
         if (tid < E) before_of[tid] = base[(size_t)first * E + tid], total_of[tid] = cnt[tid];
     } else {
-        // a thread adds two neighbours' counts in every kRows-th chunk, many in flight
-        const int half = (E + 1) / 2, lanes = half <= 64 ? 64 : half <= 128 ? 128 : 256, rows = kPlaceThr / lanes;
-        const int x = (tid & (lanes - 1)) * 2, r0 = tid / lanes;
-        int t0 = 0, t1 = 0, b0 = 0, b1 = 0;
+        // Sums of all chunks' counts fit 16 bits (kScanChunks * kTokMax tokens), so
+        // two neighbours are added as one word: a thread takes eight experts of
+        // every kPlaceThr / (E / 8)-th chunk, many in flight.
         constexpr int kU = 16;
-        if (x < E) {
-            for (int c0 = r0; c0 < chunks; c0 += kU * rows) {
-                int u[kU], v[kU];
+        if (E % 8 == 0) {
+            const int lanes = E / 8, rows = kPlaceThr / lanes, x = tid % lanes, r0 = tid / lanes;
+            uint4 t = make_uint4(0u, 0u, 0u, 0u), b = t;
+            if (r0 < rows) {
+                for (int c0 = r0; c0 < chunks; c0 += kU * rows) {
+                    uint4 v[kU];
 #pragma unroll
-                for (int i = 0; i < kU; ++i) {
-                    const int c = c0 + i * rows;
-                    const uint16_t *h = hist + (size_t)c * E + x;
-                    u[i] = c < chunks ? h[0] : 0;
-                    v[i] = c < chunks && x + 1 < E ? h[1] : 0;
+                    for (int i = 0; i < kU; ++i)
+                        v[i] = c0 + i * rows < chunks
+                                   ? *reinterpret_cast<const uint4 *>(hist + (size_t)(c0 + i * rows) * E + 8 * x)
+                                   : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int i = 0; i < kU; ++i) {
+                        t.x += v[i].x, t.y += v[i].y, t.z += v[i].z, t.w += v[i].w;
+                        if (c0 + i * rows < first) b.x += v[i].x, b.y += v[i].y, b.z += v[i].z, b.w += v[i].w;
+                    }
                 }
+                const uint32_t tw[4] = {t.x, t.y, t.z, t.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                for (int i = 0; i < kU; ++i) {
-                    t0 += u[i], t1 += v[i];
-                    if (c0 + i * rows < first) b0 += u[i], b1 += v[i];
+                for (int i = 0; i < 4; ++i) {
+                    atomicAdd(&total_of[8 * x + 2 * i], (int)(tw[i] & 0xffffu));
+                    atomicAdd(&total_of[8 * x + 2 * i + 1], (int)(tw[i] >> 16));
+                    atomicAdd(&before_of[8 * x + 2 * i], (int)(bw[i] & 0xffffu));
+                    atomicAdd(&before_of[8 * x + 2 * i + 1], (int)(bw[i] >> 16));
                 }
             }
-            atomicAdd(&total_of[x], t0);
-            atomicAdd(&before_of[x], b0);
-            if (x + 1 < E) {
-                atomicAdd(&total_of[x + 1], t1);
-                atomicAdd(&before_of[x + 1], b1);
+        } else if (tid < E) {
+            int t = 0, b = 0;
+            for (int c0 = 0; c0 < chunks; c0 += kU) {
+                int v[kU];
+#pragma unroll
+                for (int i = 0; i < kU; ++i) v[i] = c0 + i < chunks ? hist[(size_t)(c0 + i) * E + tid] : 0;
+#pragma unroll
+                for (int i = 0; i < kU; ++i) {
+                    t += v[i];
+                    if (c0 + i < first) b += v[i];
+                }
             }
+            total_of[tid] = t;
+            before_of[tid] = b;
         }
     }
     __syncthreads();
@@ -835,6 +871,7 @@ hfq_status moe_route_scored(const void *logits, hfq_dtype logits_dtype, int ld, 
     a.renorm = rule->renormalise != 0; a.scale = rule->scale;
     const int unit = a.bf16 ? 8 : 4;               // elements of 16 bytes
     a.vec = aligned16(logits) && a.ld % unit == 0 && a.size % unit == 0 && a.run % unit == 0 && a.size % a.run == 0;
+    a.bias_vec = aligned16(bias) && a.size % 4 == 0 && a.run % 4 == 0 && a.size % a.run == 0;
     cudaStream_t s = (cudaStream_t)stream;
     if (!lists) {
         // a warp a token up to one block an SM, then blocks of up to eight warps,
