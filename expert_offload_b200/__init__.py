@@ -12,6 +12,7 @@ no fallback of any kind when it is missing.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import sys
 
@@ -159,37 +160,39 @@ def _nbytes(a) -> int:
     return int(a.numel() * a.element_size())
 
 
-_I32, _I8, _ANY = 16, 17, 18               # operand types besides HFQ_F32 and HFQ_BF16
-_types = {}
+_I32, _I8, _ANY = 2, 3, 4                 # operand kinds besides HFQ_F32 and HFQ_BF16
+_ROUTE, _NORM, _QUANTIZE, _MATMUL, _LINEAR = range(5)
+_call = None
 
 
-def _operands(*ops) -> None:
-    """Checks the operands (name, tensor, type, elements): a CUDA tensor of the
-    current device (whose stream the call goes to), of that type, its last
-    dimension dense, with at least that many elements behind its address; or a
-    raw device address, which is the caller's word."""
+def _strided(name, t, n) -> None:
+    """The checks of an operand that is not simply dense and large enough."""
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise HfqError(-1, f"{name}: the elements of a row are not next to each other")
+    if t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < n:
+        raise HfqError(-1, f"{name} holds fewer than the {n} elements the call reads or writes")
+
+
+def _bind(*args) -> None:
+    """Loads and sets up the native module at the first call that finds torch."""
+    global _call
+    lib()
+    path = os.path.join(PKG, "lib", "_bind.so")
+    if not os.path.exists(path):
+        raise ImportError(f"{path} is missing: build it with `python -m expert_offload_b200.build`")
+    spec = importlib.util.spec_from_file_location("_bind", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
     torch = sys.modules.get("torch")
-    if torch is None or not torch.cuda.is_initialized():
-        device = None
+    if torch is None:
+        mod.setup(HfqError, _strided, None, None, {})
     else:
-        device = torch._C._cuda_getDevice()
-        if not _types:
-            _types.update({HFQ_F32: (torch.float32,), HFQ_BF16: (torch.bfloat16, torch.int16, torch.uint16),
-                           _I32: (torch.int32,), _I8: (torch.int8,),
-                           _ANY: (torch.uint8, torch.int8, torch.int16, torch.int32, torch.int64, torch.float32)})
-    for name, t, kind, n in ops:
-        if t is None or type(t) is int:
-            continue
-        if device is None or not isinstance(t, torch.Tensor) or t.get_device() != device:
-            raise HfqError(-1, f"{name} is neither a tensor of the current CUDA device nor a device address")
-        if t.dtype not in _types.get(kind, ()):
-            raise HfqError(-1, f"{name} is {t.dtype}, which is not the type the call names")
-        if t.is_contiguous() and t.numel() >= n:
-            continue
-        if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise HfqError(-1, f"{name}: the elements of a row are not next to each other")
-        if t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < n:
-            raise HfqError(-1, f"{name} holds fewer than the {n} elements the call reads or writes")
+        mod.setup(HfqError, _strided, torch.Tensor, torch._C._cuda_getDevice if torch.cuda.is_available() else None,
+                  {HFQ_F32: (torch.float32,), HFQ_BF16: (torch.bfloat16, torch.int16, torch.uint16),
+                   _I32: (torch.int32,), _I8: (torch.int8,),
+                   _ANY: (torch.uint8, torch.int8, torch.int16, torch.int32, torch.int64, torch.float32)})
+        _call = mod.call
+    mod.call(*args)
 
 
 def _stream(s):
@@ -261,6 +264,7 @@ class RouteRule:
     def __init__(self, score: int = SCORE_SOFTMAX, n_groups: int = 1, topk_groups: int = 1,
                  group_top: int = 1, renormalise: bool = True, scale: float = 1.0):
         self.struct = moe_route_rule(score, n_groups, topk_groups, group_top, int(renormalise), scale)
+        self.address = ctypes.addressof(self.struct)
 
 
 def moe_route_scored_workspace_bytes(T: int, E: int, k: int) -> int:
@@ -271,13 +275,14 @@ def moe_route_scored(logits, logits_dtype: int, T: int, E: int, k: int, rule: Ro
                      bias=None, cnt=None, off=None, perm=None, workspace=None, ld: int = 0,
                      stream=None) -> None:
     """Top-k routing by scores and a bias, with groups; lists as moe_route's."""
-    _operands(("logits", logits, logits_dtype, (T - 1) * (ld or E) + E), ("bias", bias, HFQ_F32, E),
-              ("idx", idx, _I32, T * k), ("wts", wts, HFQ_F32, T * k), ("cnt", cnt, _I32, E),
-              ("off", off, _I32, E + 1), ("perm", perm, _I32, T * k), ("workspace", workspace, _ANY, 0))
-    ws_bytes = _nbytes(workspace) if workspace is not None else 0
-    _check(lib().moe_route_scored(_ptr(logits), logits_dtype, ld, T, E, _ptr(bias),
-                                  ctypes.byref(rule.struct), k, _ptr(idx), _ptr(wts), _ptr(cnt),
-                                  _ptr(off), _ptr(perm), _ptr(workspace), ws_bytes, _stream(stream)))
+    (_call or _bind)(_ROUTE, ("logits", logits, logits_dtype, (T - 1) * (ld or E) + E), logits_dtype, ld, T, E,
+                     bias if bias is None else ("bias", bias, HFQ_F32, E), rule.address, k,
+                     ("idx", idx, _I32, T * k), ("wts", wts, HFQ_F32, T * k),
+                     cnt if cnt is None else ("cnt", cnt, _I32, E),
+                     off if off is None else ("off", off, _I32, E + 1),
+                     perm if perm is None else ("perm", perm, _I32, T * k),
+                     workspace if workspace is None else ("workspace", workspace, _ANY, 0),
+                     0 if workspace is None else _nbytes(workspace), _stream(stream))
 
 
 # ---------------------------------------------------- norm, gate, residual
@@ -289,26 +294,43 @@ class NormRule:
     def __init__(self, w_post=None, w_pre=None, w_dtype: int = HFQ_BF16, eps: float = 1e-6,
                  w_offset: float = 0.0, residual_scale: float = 1.0, branch_scale: float = 1.0,
                  gate_kind: int = GATE_NONE, gate_act: int = GATE_LINEAR):
-        self.w_post, self.w_pre = w_post, w_pre
+        self.w_post, self.w_pre, self.w_dtype, self.gate_kind = w_post, w_pre, w_dtype, gate_kind
         self.struct = moe_norm_rule(_ptr(w_post), _ptr(w_pre), w_dtype, eps, w_offset, residual_scale,
                                     branch_scale, gate_kind, gate_act)
+        self.address = ctypes.addressof(self.struct)
+        self.checked = 0                 # elements that the weights are known to have
+
+    def check(self, H: int) -> None:
+        """The weights hold H elements of their type on the current device; they
+        are the rule's own, so once is enough for each length."""
+        for name, w in (("w_post", self.w_post), ("w_pre", self.w_pre)):
+            if w is None or type(w) is int:
+                continue
+            torch = sys.modules.get("torch")
+            kinds = (torch.float32,) if self.w_dtype == HFQ_F32 else (torch.bfloat16, torch.int16, torch.uint16)
+            if not w.is_cuda or w.dtype not in kinds:
+                raise HfqError(-1, f"{name} is not a CUDA tensor of the rule's w_dtype")
+            _strided(name, w, H)
+        self.checked = H
 
 
 def moe_norm_residual(rule: NormRule, T: int, H: int, x, x_dtype: int, y=None, y_dtype: int = HFQ_F32,
                       y2=None, y2_gate=None, gate=None, x_out=None, xn=None, xn_dtype: int = HFQ_BF16,
                       xq=None, xq_scale=None, ldx: int = 0, ldy: int = 0, stream=None) -> None:
     """x' = residual_scale x + branch_scale gate norm(y + y2), xn = norm(x')."""
-    st = rule.struct
+    if rule.checked < H:
+        rule.check(H)
     nx, ny = (T - 1) * (ldx or H) + H, (T - 1) * (ldy or H) + H
-    _operands(("x", x, x_dtype, nx), ("y", y, y_dtype, ny), ("y2", y2, y_dtype, ny),
-              ("y2_gate", y2_gate, HFQ_F32, T),
-              ("gate", gate, HFQ_F32, {GATE_TOKEN: T, GATE_CHANNEL: H, GATE_FULL: T * H}.get(st.gate_kind, 0)),
-              ("x_out", x_out, x_dtype, nx), ("xn", xn, xn_dtype, T * H),
-              ("xq", xq, _I8, T * (-(-H // 16) * 16)), ("xq_scale", xq_scale, HFQ_F32, T),
-              ("w_post", rule.w_post, st.w_dtype, H), ("w_pre", rule.w_pre, st.w_dtype, H))
-    _check(lib().moe_norm_residual(ctypes.byref(st), T, H, _ptr(x), x_dtype, ldx, _ptr(y), _ptr(y2),
-                                   y_dtype, ldy, _ptr(y2_gate), _ptr(gate), _ptr(x_out), _ptr(xn),
-                                   xn_dtype, _ptr(xq), _ptr(xq_scale), _stream(stream)))
+    kind = rule.gate_kind
+    (_call or _bind)(_NORM, rule.address, T, H, ("x", x, x_dtype, nx), x_dtype, ldx,
+                     y if y is None else ("y", y, y_dtype, ny), y2 if y2 is None else ("y2", y2, y_dtype, ny),
+                     y_dtype, ldy, y2_gate if y2_gate is None else ("y2_gate", y2_gate, HFQ_F32, T),
+                     gate if gate is None else
+                     ("gate", gate, HFQ_F32, T if kind == GATE_TOKEN else H if kind == GATE_CHANNEL else T * H),
+                     x_out if x_out is None else ("x_out", x_out, x_dtype, nx),
+                     xn if xn is None else ("xn", xn, xn_dtype, T * H), xn_dtype,
+                     xq if xq is None else ("xq", xq, _I8, T * (-(-H // 16) * 16)),
+                     xq_scale if xq_scale is None else ("xq_scale", xq_scale, HFQ_F32, T), _stream(stream))
 
 
 # --------------------------------------------------- products in 8 bits
@@ -318,21 +340,18 @@ def q8_quantize_rows(x, x_dtype: int, rows: int, cols: int, q, scale, act: int =
     """int8 rows and their f32 scales; act ACT_SWIGLU quantises silu(gate) * up."""
     width = 2 * cols if act == ACT_SWIGLU else cols
     c16 = -(-cols // 16) * 16
-    _operands(("x", x, x_dtype, (rows - 1) * (ldx or width) + width),
-              ("q", q, _I8, (rows - 1) * (ldq or c16) + c16), ("scale", scale, HFQ_F32, rows))
-    _check(lib().q8_quantize_rows(_ptr(x), x_dtype, ldx, rows, cols, act, _ptr(q), ldq, _ptr(scale),
-                                  _stream(stream)))
+    (_call or _bind)(_QUANTIZE, ("x", x, x_dtype, (rows - 1) * (ldx or width) + width), x_dtype, ldx, rows, cols, act,
+                     ("q", q, _I8, (rows - 1) * (ldq or c16) + c16), ldq, ("scale", scale, HFQ_F32, rows),
+                     _stream(stream))
 
 
 def q8_matmul(xq, xs, T: int, K: int, wq, ws, N: int, y, y_dtype: int, ldxq: int = 0, ldw: int = 0,
               ldy: int = 0, stream=None) -> None:
     """y = (xq wq^T) * xs * ws for quantised rows xq and channels wq."""
     k16 = -(-K // 16) * 16
-    _operands(("xq", xq, _I8, (T - 1) * (ldxq or k16) + k16), ("xs", xs, HFQ_F32, T),
-              ("wq", wq, _I8, (N - 1) * (ldw or k16) + k16), ("ws", ws, HFQ_F32, N),
-              ("y", y, y_dtype, (T - 1) * (ldy or N) + N))
-    _check(lib().q8_matmul(_ptr(xq), ldxq, _ptr(xs), T, K, _ptr(wq), ldw, _ptr(ws), N, _ptr(y), y_dtype, ldy,
-                           _stream(stream)))
+    (_call or _bind)(_MATMUL, ("xq", xq, _I8, (T - 1) * (ldxq or k16) + k16), ldxq, ("xs", xs, HFQ_F32, T), T, K,
+                     ("wq", wq, _I8, (N - 1) * (ldw or k16) + k16), ldw, ("ws", ws, HFQ_F32, N), N,
+                     ("y", y, y_dtype, (T - 1) * (ldy or N) + N), y_dtype, ldy, _stream(stream))
 
 
 def q8_linear_workspace_bytes(T: int, K: int, N: int) -> int:
@@ -343,12 +362,11 @@ def q8_linear(x, x_dtype: int, T: int, K: int, wq, ws, N: int, y, y_dtype: int, 
               ldw: int = 0, ldy: int = 0, stream=None) -> None:
     """y = x W^T with x quantised on the way: q8_quantize_rows, then q8_matmul."""
     k16 = -(-K // 16) * 16
-    _operands(("x", x, x_dtype, (T - 1) * (ldx or K) + K), ("wq", wq, _I8, (N - 1) * (ldw or k16) + k16),
-              ("ws", ws, HFQ_F32, N), ("y", y, y_dtype, (T - 1) * (ldy or N) + N),
-              ("workspace", workspace, _ANY, 0))
-    ws_bytes = _nbytes(workspace) if workspace is not None else 0
-    _check(lib().q8_linear(_ptr(x), x_dtype, ldx, T, K, _ptr(wq), ldw, _ptr(ws), N, _ptr(y), y_dtype, ldy,
-                           _ptr(workspace), ws_bytes, _stream(stream)))
+    (_call or _bind)(_LINEAR, ("x", x, x_dtype, (T - 1) * (ldx or K) + K), x_dtype, ldx, T, K,
+                     ("wq", wq, _I8, (N - 1) * (ldw or k16) + k16), ldw, ("ws", ws, HFQ_F32, N), N,
+                     ("y", y, y_dtype, (T - 1) * (ldy or N) + N), y_dtype, ldy,
+                     workspace if workspace is None else ("workspace", workspace, _ANY, 0),
+                     0 if workspace is None else _nbytes(workspace), _stream(stream))
 
 
 # ---------------------------------------------------------------- forward

@@ -1,4 +1,5 @@
-"""Build step of libhfq4moe.so (nvcc for sm_100a, g++ for the host parts).
+"""Build step of libhfq4moe.so (nvcc for sm_100a, g++ for the host parts) and of
+the CPython module that calls it (gcc).
 
 Run ``python -m expert_offload_b200.build`` (or ``__graft_entry__.build()``).
 The library is written in-tree to ``expert_offload_b200/lib/``.
@@ -8,6 +9,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -16,6 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 OBJDIR = os.path.join(PKG, "lib", "obj")
 LIB = os.path.join(LIBDIR, "libhfq4moe.so")
+BIND = os.path.join(LIBDIR, "_bind.so")      # CPython module over the library (csrc/bind.c)
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -69,8 +72,15 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
                 print(" ".join(cmd), flush=True)
             subprocess.run(cmd, check=True)
     if _stale(LIB, objs):
-        cmd = [NVCC] + ARCH + ["-shared", "-cudart", "static", "-o", LIB] + objs + \
+        cmd = [NVCC] + ARCH + ["-shared", "-cudart", "static", "-Xlinker", "-soname=libhfq4moe.so", "-o", LIB] + objs + \
               ["-lpthread", "-ldl", "-lrt"]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+    src = os.path.join(CSRC, "bind.c")
+    if _stale(BIND, [src, LIB]):
+        cmd = ["gcc", "-O2", "-Wall", "-fPIC", "-shared", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+               src, "-o", BIND, LIB, "-Wl,-rpath,$ORIGIN"]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)

@@ -105,8 +105,8 @@ def _route(lib, dtype=0, ld=0, T=4, E=64, k=8, n=8, tg=4, gt=2, score=1, scale=1
     (dict(n=7), -3), (dict(n=64), -3), (dict(n=0), -3), (dict(tg=0), -1), (dict(tg=9), -1), (dict(gt=3), -1),
     (dict(gt=0), -1), (dict(E=32, n=32, tg=32, gt=2), -1), (dict(k=9, tg=1), -1), (dict(score=2), -1),
     (dict(scale=float("inf")), -1), (dict(scale=float("nan")), -1), (dict(logits=A + 2), -2), (dict(bias=A + 1), -2),
-    (dict(dtype=1, logits=A + 1), -2), (dict(lists=(A, A, None)), -1), (dict(lists=(A, A, A)), -8),
-    (dict(lists=(A, A, A), ws=A, wsb=16), -8), (dict(lists=(A, A, A), ws=A + 4, wsb=1 << 20), -2),
+    (dict(dtype=1, logits=A + 1), -2), (dict(lists=(A, A, None)), -1), (dict(lists=(A, A, A), T=40), -8),
+    (dict(lists=(A, A, A), T=40, ws=A, wsb=16), -8), (dict(lists=(A, A, A), T=40, ws=A + 4, wsb=1 << 20), -2),
     (dict(wts=A + 2), -2)])
 def test_route_refusals(lib, kw, status):
     assert _route(lib, **kw) == status
@@ -179,6 +179,28 @@ def test_matmul_refusals(lib, kw, status):
     d.update(kw)
     assert lib.q8_matmul(*d.values(), None) == status
     assert eo.last_error()
+
+
+def test_route_workspace_bytes(lib):
+    f = lib.moe_route_scored_workspace_bytes
+    assert f(16, 256, 8) == 0 and f(0, 256, 8) == 0       # up to 16 tokens: one block, no workspace
+    assert f(17, 256, 8) >= 2 * 3 * 256
+    for T in (1184, 1185, 2368, 2369, 8192, 8193, 65536):
+        assert f(T, 512, 8) % 4 == 0 and f(T, 512, 8) >= 2 * 512 * (T // 32)
+
+
+def test_binding_checks_sizes_and_raw_addresses(lib):
+    with pytest.raises(eo.HfqError) as e:
+        eo.q8_quantize_rows(A, eo.HFQ_F32, 2 ** 32 + 4, 64, A, A)
+    assert e.value.status == -1 and "range" in e.value.message
+    with pytest.raises(eo.HfqError) as e:
+        eo.q8_quantize_rows(A, eo.HFQ_F32, 4, 64, A + 4, A)
+    assert e.value.status == -2 and "q must be 16-byte aligned" in e.value.message
+    with pytest.raises(TypeError):
+        eo.q8_quantize_rows(A, eo.HFQ_F32, 4.5, 64, A, A)
+    with pytest.raises(eo.HfqError) as e:
+        eo.moe_norm_residual(eo.NormRule(), 4, 64, A, 9, xn=A)
+    assert e.value.status == -1
 
 
 def test_binding_refuses_tensors_it_cannot_use():
