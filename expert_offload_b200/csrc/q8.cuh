@@ -1,6 +1,8 @@
 // q8.cuh - what the 8-bit product's translation units share.
 #pragma once
 
+#include <atomic>
+
 #include "quant8.cuh"
 
 namespace hfq {
@@ -24,6 +26,20 @@ hfq_status launch_q8_tc(const Q8Mat &a, bool chained, cudaStream_t s);
 // The same for up to 8 tokens that come as they are, quantised on the way.
 constexpr int kQ8FusedTokens = 8;
 hfq_status launch_q8_fused(const Q8Mat &a, const void *x, bool x_bf16, size_t ldx, cudaStream_t s);
+// Lets kernel f use `bytes` of dynamic shared memory on the current device, once
+// for each device (`done`: a bit for each, the first 64).
+inline cudaError_t allow_smem(const void *f, int bytes, std::atomic<unsigned long long> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 // Status word of its bounded waits on the current device; clears it.
 hfq_status q8_status(cudaStream_t s);
 

@@ -87,12 +87,12 @@ struct Args {
     Q8Mat m;
     const void *x;                        // fused: the tokens as they are, rows ldx elements apart
     size_t ldx;
-    int x_bf16, x_vec;
+    int x_vec;
     long long timeout_ns;
     int stages;                           // of the tile kernel's ring
     int split;                            // CTAs of a cluster, each with a share of K (two stages at least)
     int share;                            // stages of K that a CTA of the cluster takes at most
-    int chained;                          // weights may be read before the dependency wait
+    int chained;                          // launched behind the quantiser, beside which it may start
     int hook;                             // test hook: the MMA warp waits for an arrival that never comes
 };
 
@@ -202,19 +202,23 @@ constexpr int kFew = 16;                  // tokens of its tile
 constexpr int kShare = 24;                // its stages of K: 48 KB of quantised tokens
 constexpr int kQuantWarps = 8;
 
-template <int BT, bool FUSED>
+enum { kPlain = 0, kFusedBf16 = 1, kFusedF32 = 2 };
+
+template <int BT, int MODE>
 struct TileCfg {
+    static constexpr bool FUSED = MODE != kPlain;
     static constexpr int kA = kCh * kKb, kB = BT * kKb, kStage = FUSED ? kA : kA + kB;
     static constexpr int kExch = kCh * BT * 4;                       // bytes of the exchange
     static constexpr int kThr = FUSED ? 64 + 32 * kQuantWarps : 192; // TMA warp, MMA warp, the others
     static constexpr uint32_t kCols = BT < 32 ? 32 : BT;             // tensor-memory columns
 };
 
-template <int BT, bool FUSED>
-__global__ void __launch_bounds__(TileCfg<BT, FUSED>::kThr)
+template <int BT, int MODE>
+__global__ void __launch_bounds__(TileCfg<BT, MODE>::kThr)
 q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap)
 {
-    using C = TileCfg<BT, FUSED>;
+    using C = TileCfg<BT, MODE>;
+    constexpr bool FUSED = C::FUSED, BF16 = MODE == kFusedBf16;
     extern __shared__ uint8_t raw[];
     uint8_t *buf = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     uint8_t *xbuf = buf + a.stages * C::kStage;                      // FUSED: [share][kB]
@@ -245,6 +249,12 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
         fence_mbar_init();
         if (FUSED && a.split > 1) mbar_arrive_expect_tx(&amax_bar, (uint32_t)(a.split * m.T * 4));
         abort_flag = 0;
+        // the first weights set out before anything else is done (where the kernel
+        // may run beside the quantiser, that one started after all that wrote them)
+        for (int j = 0; j < min(stages, c1 - c0); ++j) {
+            mbar_arrive_expect_tx(&full[j], C::kStage);
+            tma_load_2d(buf + j * C::kStage, &wmap, (c0 + j) * kKb, n0, &full[j]);
+        }
     }
     if (warp == 1) {
         tmem_alloc(&tmem_base, C::kCols);
@@ -259,27 +269,19 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
 
     if (warp == 0) {
         if (lane == 0) {
-            int issued = 0, s = -1, round = 0;               // issued = round * stages + s + 1
-            bool waited = false;
-            if (!a.chained) {
+            int issued = min(stages, c1 - c0), s = 0, round = 1;
+            if (!FUSED) {
                 grid_dependency_wait();
-                waited = true;
+                for (int j = 0; j < issued; ++j)
+                    tma_load_2d(buf + j * C::kStage + C::kA, &xmap, (c0 + j) * kKb, t0, &full[j]);
             }
-            for (int c = c0; c < c1; ++c, ++issued) {
-                if (++s == stages) s = 0, ++round;
-                if (round > 0 && !wait_bar(&empty[s], (uint32_t)(round - 1) & 1u, a.timeout_ns, abortp)) break;
+            for (; issued < c1 - c0; ++issued) {
+                if (!wait_bar(&empty[s], (uint32_t)(round - 1) & 1u, a.timeout_ns, abortp)) break;
                 uint8_t *dst = buf + s * C::kStage;
                 mbar_arrive_expect_tx(&full[s], C::kStage);
-                tma_load_2d(dst, &wmap, c * kKb, n0, &full[s]);
-                if (FUSED) continue;
-                if (!waited && (issued == stages - 1 || c == c1 - 1)) {
-                    // the first stages' weights are on their way: now the tokens
-                    grid_dependency_wait();
-                    waited = true;
-                    for (int j = 0; j <= issued; ++j)
-                        tma_load_2d(buf + j * C::kStage + C::kA, &xmap, (c0 + j) * kKb, t0, &full[j]);
-                } else if (waited)
-                    tma_load_2d(dst + C::kA, &xmap, c * kKb, t0, &full[s]);
+                tma_load_2d(dst, &wmap, (c0 + issued) * kKb, n0, &full[s]);
+                if (!FUSED) tma_load_2d(dst + C::kA, &xmap, (c0 + issued) * kKb, t0, &full[s]);
+                if (++s == stages) s = 0, ++round;
             }
             // every copy has landed before the CTA may end
             for (int i = max(0, issued - stages); i < issued; ++i)
@@ -308,44 +310,54 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
         __syncwarp();
         if (a.split > 1) cluster_wait();
     } else {
-        if (a.split > 1) cluster_wait();
+        if (!FUSED && a.split > 1) cluster_wait();
         if (FUSED) {
-            const int k0 = c0 * kKb, k1 = min(m.K, c1 * kKb);
-            for (int t = warp - 2; t < m.T; t += kQuantWarps) {
-                const void *row = row_at(a.x, a.x_bf16, (size_t)t * a.ldx);
-                uint32_t big = 0;
-                for (int k = k0 + 8 * lane; k < k1; k += 256) {
-                    float v[8];
-                    load8(row, a.x_bf16, a.x_vec, k, k1, v);
+            // A token is one warp's.  The code is kept short (rolled loops, one type
+            // for each instantiation): a launch runs it once, from cold instruction
+            // caches, and unrolled it cost more than its work.
+            const int k0 = c0 * kKb, k1 = min(m.K, c1 * kKb), t = warp - 2;
+            const void *row = row_at(a.x, BF16, (size_t)t * a.ldx);
+            const bool mine = t < m.T;
+            uint32_t big = 0;
+            if (mine) {
+                if (a.x_vec) {                               // whole 16-byte pieces, four requested at a time
+#pragma unroll 1
+                    for (int k = k0 + 8 * lane; k < k1; k += 1024) {
+                        Raw8 r[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) big = max(big, abs_bits(v[e]));
+                        for (int u = 0; u < 4; ++u) {
+                            r[u].a = r[u].b = make_uint4(0u, 0u, 0u, 0u);
+                            if (k + 256 * u < k1) r[u] = load_raw8<BF16>(row, k + 256 * u);
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) big = max(big, raw_max<BF16>(r[u]));
+                    }
+                } else {
+#pragma unroll 1
+                    for (int k = k0 + lane; k < k1; k += 32)
+                        big = max(big, abs_bits(load_act(row, BF16 ? HFQ_BF16 : HFQ_F32, k)));
                 }
                 big = __reduce_max_sync(0xffffffffu, big);
-                if (a.split == 1) {
-                    if (lane == 0) top[t] = big;
-                } else if (lane < a.split)
-                    st_async(map_rank(smem_u32(&top_in[rank][t]), (uint32_t)lane), big,
-                             map_rank(smem_u32(&amax_bar), (uint32_t)lane));
             }
             __syncwarp();
-            if (a.split > 1) {
-                wait_bar(&amax_bar, 0u, a.timeout_ns, abortp);
-                for (int t = warp - 2; t < m.T; t += kQuantWarps) {
-                    const uint32_t big = __reduce_max_sync(0xffffffffu, lane < a.split ? top_in[lane][t] : 0u);
-                    if (lane == 0) top[t] = big;
+            if (a.split > 1) cluster_wait();                 // the other CTAs have set up their barriers
+            if (mine) {
+                if (a.split > 1) {
+                    if (lane < a.split)
+                        st_async(map_rank(smem_u32(&top_in[rank][t]), (uint32_t)lane), big,
+                                 map_rank(smem_u32(&amax_bar), (uint32_t)lane));
+                    wait_bar(&amax_bar, 0u, a.timeout_ns, abortp);
+                    big = __reduce_max_sync(0xffffffffu, lane < a.split ? top_in[lane][t] : 0u);
                 }
-                __syncwarp();
-            }
-            for (int t = warp - 2; t < m.T; t += kQuantWarps) {
-                const void *row = row_at(a.x, a.x_bf16, (size_t)t * a.ldx);
-                const RowQuant<true> qb(top[t]);
-                const RowQuant<false> qf(top[t]);
+                if (lane == 0) top[t] = big;
+                const RowQuant<BF16> q(big);
+#pragma unroll 1
                 for (int k = k0 + 8 * lane; k < k1; k += 256) {
                     float v[8];
-                    load8(row, a.x_bf16, a.x_vec, k, k1, v);
+                    load8(row, BF16, a.x_vec, k, k1, v);
                     // row t of the tile, 16-byte piece (k / 16) % 8 at its swizzled place
                     uint8_t *at = xbuf + (k - k0) / kKb * C::kB + t * kKb + ((((k >> 4) & 7) ^ (t & 7)) << 4) + (k & 8);
-                    *reinterpret_cast<uint2 *>(at) = a.x_bf16 ? qb(v) : qf(v);
+                    *reinterpret_cast<uint2 *>(at) = q(v);
                 }
             }
             fence_proxy_async_smem();                        // the MMAs read through the async proxy
@@ -647,12 +659,13 @@ bool encode(CUtensorMap *map, const int8_t *base, int K, int rows, size_t ld, in
                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int BT, bool FUSED>
+template <int BT, int MODE>
 cudaError_t launch_tile(Args a, const CUtensorMap &wmap, const CUtensorMap &xmap, cudaStream_t s)
 {
-    using C = TileCfg<BT, FUSED>;
-    const cudaError_t e = cudaFuncSetAttribute(q8_tile_kernel<BT, FUSED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kSmemFull);
+    using C = TileCfg<BT, MODE>;
+    constexpr bool FUSED = C::FUSED;
+    static std::atomic<unsigned long long> allowed{0};
+    const cudaError_t e = allow_smem((const void *)q8_tile_kernel<BT, MODE>, kSmemFull, allowed);
     if (e != cudaSuccess) return e;
     // as many stages as K has, and as fit with one CTA or two on an SM (two for
     // clusters: eight CTAs that need an SM each do not find room in every GPC)
@@ -674,14 +687,15 @@ cudaError_t launch_tile(Args a, const CUtensorMap &wmap, const CUtensorMap &xmap
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = a.chained ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, q8_tile_kernel<BT, FUSED>, a, wmap, xmap);
+    return cudaLaunchKernelEx(&cfg, q8_tile_kernel<BT, MODE>, a, wmap, xmap);
 }
 
 cudaError_t launch_pair(const Args &a, const CUtensorMap &wmap, const CUtensorMap &xmap, cudaStream_t s)
 {
     using C = PairCfg;
     constexpr int BT = C::kBT;
-    cudaError_t e = cudaFuncSetAttribute(q8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static std::atomic<unsigned long long> allowed{0};
+    const cudaError_t e = allow_smem((const void *)q8_pair_kernel, C::kSmem, allowed);
     if (e != cudaSuccess) return e;
     const int tiles = (a.m.N + 2 * kCh - 1) / (2 * kCh) * ((a.m.T + BT - 1) / BT);
     cudaLaunchConfig_t cfg = {};
@@ -721,8 +735,7 @@ hfq_status launch_q8_fused(const Q8Mat &m, const void *x, bool x_bf16, size_t ld
     a.m = m;
     a.x = x;
     a.ldx = ldx;
-    a.x_bf16 = x_bf16;
-    a.x_vec = aligned16(x) && ldx * (x_bf16 ? 2 : 4) % 16 == 0;
+    a.x_vec = aligned16(x) && ldx * (x_bf16 ? 2 : 4) % 16 == 0 && m.K % 8 == 0;
     a.timeout_ns = option_wait_timeout_ns();
     a.hook = option_take_extra_arrivals();
     const int nk = (m.K + kKb - 1) / kKb;
@@ -731,7 +744,7 @@ hfq_status launch_q8_fused(const Q8Mat &m, const void *x, bool x_bf16, size_t ld
     CUtensorMap wmap;
     if (!encode(&wmap, m.wq, m.K, m.N, m.ldw, kCh))
         return fail(HFQ_ERR_CUDA, "8-bit product: tensor map encoding failed (K %d, N %d)", m.K, m.N);
-    cudaError_t e = launch_tile<kFew, true>(a, wmap, wmap, s);
+    cudaError_t e = x_bf16 ? launch_tile<kFew, kFusedBf16>(a, wmap, wmap, s) : launch_tile<kFew, kFusedF32>(a, wmap, wmap, s);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "8-bit product launch: %s", cudaGetErrorString(e));
     return HFQ_OK;
@@ -758,10 +771,10 @@ hfq_status launch_q8_tc(const Q8Mat &m, bool chained, cudaStream_t s)
         return fail(HFQ_ERR_CUDA, "8-bit product: tensor map encoding failed (T %d, K %d, N %d)", m.T, m.K, m.N);
     a.split = split_of(bt, ct * ((m.T + bt - 1) / bt), nk);
     cudaError_t e = pair       ? launch_pair(a, wmap, xmap, s)
-                    : bt == 16 ? launch_tile<16, false>(a, wmap, xmap, s)
-                    : bt == 32 ? launch_tile<32, false>(a, wmap, xmap, s)
-                    : bt == 64 ? launch_tile<64, false>(a, wmap, xmap, s)
-                               : launch_tile<128, false>(a, wmap, xmap, s);
+                    : bt == 16 ? launch_tile<16, kPlain>(a, wmap, xmap, s)
+                    : bt == 32 ? launch_tile<32, kPlain>(a, wmap, xmap, s)
+                    : bt == 64 ? launch_tile<64, kPlain>(a, wmap, xmap, s)
+                               : launch_tile<128, kPlain>(a, wmap, xmap, s);
     if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "8-bit product launch: %s", cudaGetErrorString(e));
     return HFQ_OK;

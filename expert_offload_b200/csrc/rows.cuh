@@ -38,6 +38,20 @@ __device__ __forceinline__ void expand8(const Raw8 &r, float (&v)[8])
 // Rounds v to bf16 (as a float).
 __device__ __forceinline__ float round_bf16(float v) { return bf16_bits_to_float(float_to_bf16_bits(v)); }
 
+// The largest magnitude of eight elements, as f32 bits.
+template <bool BF16>
+__device__ __forceinline__ uint32_t raw_max(const Raw8 &r)
+{
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < (BF16 ? 4 : 8); ++i) {
+        m = max(m, w[i] & (BF16 ? 0x7fff0000u : 0x7fffffffu));
+        if (BF16) m = max(m, (w[i] & 0x7fffu) << 16);
+    }
+    return m;
+}
+
 // Elements [c, c + 8) of a row of n (0 behind it): one or two 16-byte loads
 // where the row allows them (`vec`: it starts on 16 bytes), else one by one.
 __device__ __forceinline__ void load8(const void *row, bool bf16, bool vec, int c, int n, float (&v)[8])
