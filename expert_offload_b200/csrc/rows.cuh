@@ -18,7 +18,7 @@ __device__ __forceinline__ Raw8 load_raw8(const void *p, size_t i)
     Raw8 r;
     if (BF16) {
         r.a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
-        r.b = r.a;
+        r.b = make_uint4(0u, 0u, 0u, 0u);
     } else {
         r.a = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i)[0];
         r.b = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i)[1];

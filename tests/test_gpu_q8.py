@@ -78,6 +78,36 @@ def test_quantiser_borders_and_ranges(eo):
     assert (q[:4, :100] == 0).all() and s[0] == 0 and torch.isnan(s[1:4]).all() and (s[4:] > 0).all()
 
 
+def test_every_bf16_quotient(eo):
+    """Each significand of a row's largest value against each significand of a
+    value, over the binary places in which a quotient of 1/2 or more can lie:
+    all the quotients that bf16 rows have, exact halves among them."""
+    sig = np.arange(128, 256, dtype=np.float64)
+    v = np.concatenate([sig * 2.0 ** -d for d in range(11)])
+    for e in (-7, 60):
+        rows = np.zeros((128, len(v) + 1))
+        for r, top in enumerate(sig):
+            rows[r, 1:] = np.where(v <= top, v, 0) * np.where(np.arange(len(v)) % 2, 1, -1)
+            rows[r, 0] = top
+        x = torch.from_numpy(rows * 2.0 ** e).bfloat16().cuda()
+        assert torch.equal(x.double().cpu(), torch.from_numpy(rows * 2.0 ** e))      # all of them bf16 values
+        q, s = _quantise(eo, x, 128, rows.shape[1], "bf16")
+        rq, rs = q8.quantise((rows * 2.0 ** e).astype(np.float32))
+        np.testing.assert_array_equal(q[:, :rows.shape[1]].cpu().numpy(), rq)
+        np.testing.assert_array_equal(s.cpu().numpy(), rs)
+        y = torch.empty(128, 16, device="cuda")          # the fused quantisers' bits, a row at a time
+        eye, one = torch.eye(16, 1424, dtype=torch.int8, device="cuda"), torch.ones(16, device="cuda")
+        for cols in range(0, 1408, 352):
+            part = torch.cat([x[:, :1], x[:, 1 + cols:1 + cols + 15]], 1).contiguous()
+            for r in range(0, 128, 5):
+                n = min(5, 128 - r)
+                eo.q8_linear(part[r:r + n], eo.HFQ_BF16, n, 16, eye, one, 16, y[r:r + n], eo.HFQ_F32,
+                             torch.zeros(1 << 16, dtype=torch.uint8, device="cuda"), ldw=1424)
+            pq, ps = q8.quantise(part.float().cpu().numpy())
+            torch.cuda.synchronize()
+            np.testing.assert_array_equal(y.cpu().numpy(), pq.astype(np.float32) * ps[:, None])
+
+
 @pytest.mark.parametrize("rows,cols,ldx,ldq,shift", [(4, 100, 103, 128, 1), (4, 64, 72, 64, 0), (3, 4096, 4100, 4112, 3),
                                                      (2, 2048, 2049, 2048, 0)])
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
