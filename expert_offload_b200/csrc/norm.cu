@@ -12,6 +12,7 @@
 #include <algorithm>
 #include <cfloat>
 
+#include "launch.cuh"
 #include "rows.cuh"
 
 namespace hfq {
@@ -346,6 +347,7 @@ template <bool VEC, int NV, bool XB, bool YB>
 __global__ void __launch_bounds__(NV * 256, NV > 1 ? 2 : VEC ? 5 : 3) norm_kernel(const Args a)
 {
     __shared__ __align__(16) float red[kReds][kMaxWarps];
+    begin_ordered();
     // rows of one warp share blocks; others have one of their own
     const int nt = a.packed ? 32 : blockDim.x, sub = a.packed ? threadIdx.x >> 5 : 0;
     const int t = a.packed ? blockIdx.x * kPacked + sub : blockIdx.x;
@@ -365,14 +367,14 @@ __global__ void __launch_bounds__(NV * 256, NV > 1 ? 2 : VEC ? 5 : 3) norm_kerne
 }
 
 template <bool VEC, int NV>
-void launch(Args a, bool xb, bool yb, int nt, cudaStream_t s)
+cudaError_t launch(Args a, bool xb, bool yb, int nt, cudaStream_t s)
 {
     a.packed = nt == 32 && a.T > 148;
     const int rows = a.packed ? kPacked : 1, grid = (a.T + rows - 1) / rows, block = nt * rows;
-    if (xb && yb) norm_kernel<VEC, NV, true, true><<<grid, block, 0, s>>>(a);
-    else if (xb) norm_kernel<VEC, NV, true, false><<<grid, block, 0, s>>>(a);
-    else if (yb) norm_kernel<VEC, NV, false, true><<<grid, block, 0, s>>>(a);
-    else norm_kernel<VEC, NV, false, false><<<grid, block, 0, s>>>(a);
+    if (xb && yb) return launch_ordered(norm_kernel<VEC, NV, true, true>, grid, block, 0, s, a);
+    if (xb) return launch_ordered(norm_kernel<VEC, NV, true, false>, grid, block, 0, s, a);
+    if (yb) return launch_ordered(norm_kernel<VEC, NV, false, true>, grid, block, 0, s, a);
+    return launch_ordered(norm_kernel<VEC, NV, false, false>, grid, block, 0, s, a);
 }
 
 bool finite(float v) { return v >= -FLT_MAX && v <= FLT_MAX; }
@@ -435,14 +437,8 @@ extern "C" hfq_status moe_norm_residual(const moe_norm_rule *rule, int T, int H,
     const bool xb = x_dtype == HFQ_BF16, yb = y_dtype == HFQ_BF16;
     cudaStream_t s = (cudaStream_t)stream;
     auto threads = [&](int per) { return ((H + per - 1) / per + 31) / 32 * 32; };
-    if (H <= 2048) {
-        if (vec) launch<true, 1>(a, xb, yb, threads(8), s);
-        else launch<false, 1>(a, xb, yb, threads(8), s);
-    } else {
-        if (vec) launch<true, 2>(a, xb, yb, threads(16), s);
-        else launch<false, 2>(a, xb, yb, threads(16), s);
-    }
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = H <= 2048 ? (vec ? launch<true, 1>(a, xb, yb, threads(8), s) : launch<false, 1>(a, xb, yb, threads(8), s))
+                                      : (vec ? launch<true, 2>(a, xb, yb, threads(16), s) : launch<false, 2>(a, xb, yb, threads(16), s));
     if (err != cudaSuccess) return fail(HFQ_ERR_CUDA, "moe_norm_residual launch: %s", cudaGetErrorString(err));
     return ok();
 }

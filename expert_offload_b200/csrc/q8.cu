@@ -2,6 +2,7 @@
 // output channel: q8_quantize_rows, q8_matmul, q8_linear.
 #include <algorithm>
 
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "q8.cuh"
 #include "rows.cuh"
@@ -17,7 +18,6 @@ struct QuantArgs {
     size_t ldx, ldq;
     int rows, cols, bf16, swiglu, vec;
     int per_row;                 // threads of a row, a power of two of at least 32
-    int early;                   // the next kernel may start before this one ends
 };
 
 // A row is read once: `per_row` threads hold it in registers, NV chunks of 8
@@ -50,10 +50,10 @@ __device__ __forceinline__ uint32_t row_top(const QuantArgs &a, uint32_t top, ui
 }
 
 template <int NV, bool BF16>
-__global__ void __launch_bounds__(512, 2) quantize_vec_kernel(const QuantArgs a)
+__global__ void __launch_bounds__(512, 2) quantize_vec_kernel(QuantArgs a)
 {
     __shared__ uint32_t red[16];
-    if (a.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_ordered();
     const int j = threadIdx.x & (a.per_row - 1);
     const size_t r = (size_t)blockIdx.x * (blockDim.x / a.per_row) + threadIdx.x / a.per_row;
     const bool in = r < (size_t)a.rows;
@@ -81,10 +81,10 @@ __global__ void __launch_bounds__(512, 2) quantize_vec_kernel(const QuantArgs a)
 }
 
 template <int NV, bool EXACT>
-__global__ void __launch_bounds__(512) quantize_kernel(const QuantArgs a)
+__global__ void __launch_bounds__(512) quantize_kernel(QuantArgs a)
 {
     __shared__ uint32_t red[16];
-    if (a.early) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_ordered();
     const int j = threadIdx.x & (a.per_row - 1);
     const size_t r = (size_t)blockIdx.x * (blockDim.x / a.per_row) + threadIdx.x / a.per_row;
     const bool in = r < (size_t)a.rows;
@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kDotWarps * 32) dot_kernel(const DotArgs a)
     __shared__ uint32_t top[TT];
     const Q8Mat &m = a.m;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    begin_ordered();
     const int n0 = (blockIdx.x * kDotWarps + warp) * R;
     const int k16 = (int)round16(m.K), kp = (m.K + 511) / 512 * 512;
     auto load = [&](int r, int k) {
@@ -272,28 +273,23 @@ hfq_status check_out(const char *who, int T, int K, const int8_t *wq, int ldw, c
     return check_q(who, "wq", wq, ldw, K);
 }
 
-void launch_quantize(const void *x, bool bf16, size_t ldx, int rows, int cols, bool swiglu, int8_t *q, size_t ldq,
-                     float *scale, bool early, cudaStream_t s)
+cudaError_t launch_quantize(const void *x, bool bf16, size_t ldx, int rows, int cols, bool swiglu, int8_t *q, size_t ldq,
+                            float *scale, cudaStream_t s)
 {
-    QuantArgs a{x, q, scale, ldx, ldq, rows, cols, bf16, swiglu, 0, 32, early};
+    QuantArgs a{x, q, scale, ldx, ldq, rows, cols, bf16, swiglu, 0, 32};
     const size_t size = bf16 ? 2 : 4;
     // rows at 16-byte addresses, of whole 8-element pieces
     a.vec = aligned16(x) && ldx * size % 16 == 0 && cols % 8 == 0;
     const int nv = cols <= 4096 ? 2 : 4;
     while (a.per_row * 8 * nv < cols) a.per_row *= 2;      // at most 512
     const int block = std::max(a.per_row, 256), per = block / a.per_row, grid = (rows + per - 1) / per;
-    if (a.vec && !swiglu) {
-        if (nv == 2 && bf16) quantize_vec_kernel<2, true><<<grid, block, 0, s>>>(a);
-        else if (nv == 2) quantize_vec_kernel<2, false><<<grid, block, 0, s>>>(a);
-        else if (bf16) quantize_vec_kernel<4, true><<<grid, block, 0, s>>>(a);
-        else quantize_vec_kernel<4, false><<<grid, block, 0, s>>>(a);
-    } else {
-        const bool exact = bf16 && !swiglu;
-        if (nv == 2 && exact) quantize_kernel<2, true><<<grid, block, 0, s>>>(a);
-        else if (nv == 2) quantize_kernel<2, false><<<grid, block, 0, s>>>(a);
-        else if (exact) quantize_kernel<4, true><<<grid, block, 0, s>>>(a);
-        else quantize_kernel<4, false><<<grid, block, 0, s>>>(a);
-    }
+    void (*kernel)(QuantArgs);
+    if (a.vec && !swiglu)
+        kernel = nv == 2 ? (bf16 ? quantize_vec_kernel<2, true> : quantize_vec_kernel<2, false>)
+                         : (bf16 ? quantize_vec_kernel<4, true> : quantize_vec_kernel<4, false>);
+    else if (bf16 && !swiglu) kernel = nv == 2 ? quantize_kernel<2, true> : quantize_kernel<4, true>;
+    else kernel = nv == 2 ? quantize_kernel<2, false> : quantize_kernel<4, false>;
+    return launch_ordered(kernel, grid, block, 0, s, a);
 }
 
 template <int TT, int R>
@@ -304,8 +300,7 @@ cudaError_t launch_dot(const DotArgs &a, int smem, cudaStream_t s)
         if (e != cudaSuccess) return e;
     }
     const int per = kDotWarps * R;
-    dot_kernel<TT, R><<<(a.m.N + per - 1) / per, kDotWarps * 32, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_ordered(dot_kernel<TT, R>, (a.m.N + per - 1) / per, kDotWarps * 32, smem, s, a);
 }
 
 // One or two tokens and few weights: the dot kernel's short start wins (2.9 us
@@ -347,9 +342,8 @@ hfq_status q8_quantize_rows(const void *x, hfq_dtype x_dtype, int ldx, int rows,
     if (st) return st;
     if ((st = check_q("q8_quantize_rows", "q", q, ldq, cols))) return st;
     if (misaligned(scale, HFQ_F32)) return fail(HFQ_ERR_ALIGN, "q8_quantize_rows: scale must be 4-byte aligned");
-    launch_quantize(x, x_dtype == HFQ_BF16, ldx ? ldx : width, rows, cols, act == HFQ_ACT_SWIGLU, q,
-                    ldq ? ldq : round16(cols), scale, false, (cudaStream_t)stream);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = launch_quantize(x, x_dtype == HFQ_BF16, ldx ? ldx : width, rows, cols, act == HFQ_ACT_SWIGLU, q,
+                                            ldq ? ldq : round16(cols), scale, (cudaStream_t)stream);
     if (err != cudaSuccess) return fail(HFQ_ERR_CUDA, "q8_quantize_rows launch: %s", cudaGetErrorString(err));
     return ok();
 }
@@ -400,8 +394,7 @@ hfq_status q8_linear(const void *x, hfq_dtype x_dtype, int ldx, int T, int K, co
     } else {
         int8_t *xq = static_cast<int8_t *>(workspace);
         float *xs = reinterpret_cast<float *>(xq + ((size_t)T * round16(K) + 255) / 256 * 256);
-        launch_quantize(x, bf16, ld, T, K, false, xq, round16(K), xs, true, s);
-        const cudaError_t err = cudaGetLastError();
+        const cudaError_t err = launch_quantize(x, bf16, ld, T, K, false, xq, round16(K), xs, s);
         if (err != cudaSuccess) return fail(HFQ_ERR_CUDA, "q8_linear launch: %s", cudaGetErrorString(err));
         m.xq = xq;
         m.xs = xs;

@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "launch.cuh"
 #include "ptx.cuh"
 #include "q8.cuh"
 #include "rows.cuh"
@@ -78,10 +79,6 @@ __device__ __forceinline__ void st_async(uint32_t addr, uint32_t v, uint32_t bar
                  "r"(bar)
                  : "memory");
 }
-
-// Work that another kernel launched before this one on the stream may still
-// be doing: waits until it has finished and its writes are visible.
-__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 struct Args {
     Q8Mat m;
@@ -249,8 +246,10 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
         fence_mbar_init();
         if (FUSED && a.split > 1) mbar_arrive_expect_tx(&amax_bar, (uint32_t)(a.split * m.T * 4));
         abort_flag = 0;
-        // the first weights set out before anything else is done (where the kernel
-        // may run beside the quantiser, that one started after all that wrote them)
+        // The first weights set out before anything else is done: behind the
+        // quantiser without waiting for it, since it has let this kernel begin only
+        // after all that might have written them had ended.
+        if (!a.chained) dependency_wait();
         for (int j = 0; j < min(stages, c1 - c0); ++j) {
             mbar_arrive_expect_tx(&full[j], C::kStage);
             tma_load_2d(buf + j * C::kStage, &wmap, (c0 + j) * kKb, n0, &full[j]);
@@ -264,17 +263,17 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
     __syncthreads();
     tc_fence_after_sync();
     if (a.split > 1) cluster_arrive();    // waited for before this CTA touches another's shared memory
+    dependency_wait();
+    let_next_begin();
     const uint32_t tmem = tmem_base;
     volatile int *abortp = &abort_flag;
 
     if (warp == 0) {
         if (lane == 0) {
             int issued = min(stages, c1 - c0), s = 0, round = 1;
-            if (!FUSED) {
-                grid_dependency_wait();
+            if (!FUSED)
                 for (int j = 0; j < issued; ++j)
                     tma_load_2d(buf + j * C::kStage + C::kA, &xmap, (c0 + j) * kKb, t0, &full[j]);
-            }
             for (; issued < c1 - c0; ++issued) {
                 if (!wait_bar(&empty[s], (uint32_t)(round - 1) & 1u, a.timeout_ns, abortp)) break;
                 uint8_t *dst = buf + s * C::kStage;
@@ -374,7 +373,6 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
             const int tv = min(BT, m.T - t0);
             if (__all_sync(0xffffffffu, ok)) {
                 if (a.split == 1) {
-                    if (!FUSED) grid_dependency_wait();      // xs comes from the kernel before, too
                     const bool pairs = m.y_bf16 && m.ldy % 2 == 0 && ((uintptr_t)m.y & 3) == 0;
                     const float ws = n < m.N ? m.ws[n] : 0.0f;
 #pragma unroll 1
@@ -410,7 +408,6 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
     if (a.split > 1) {
         __syncwarp();
         cluster_sync();
-        if (!FUSED) grid_dependency_wait();
         const int own = kCh / a.split, tv = min(BT, m.T - t0);
         const int4 *part = reinterpret_cast<const int4 *>(ebuf);
         for (int i = threadIdx.x; i < own * ((tv + 3) / 4); i += C::kThr) {
@@ -545,7 +542,8 @@ q8_pair_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
     tc_fence_after_sync();
     const uint32_t tmem = tmem_base;
     volatile int *abortp = &abort_flag;
-    grid_dependency_wait();
+    dependency_wait();
+    let_next_begin();
 
     if (warp == 0 && lane == 0) {
         int g = 0;                                       // stages filled so far
@@ -686,7 +684,7 @@ cudaError_t launch_tile(Args a, const CUtensorMap &wmap, const CUtensorMap &xmap
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = a.chained ? 2 : 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, q8_tile_kernel<BT, MODE>, a, wmap, xmap);
 }
 
@@ -698,17 +696,7 @@ cudaError_t launch_pair(const Args &a, const CUtensorMap &wmap, const CUtensorMa
     const cudaError_t e = allow_smem((const void *)q8_pair_kernel, C::kSmem, allowed);
     if (e != cudaSuccess) return e;
     const int tiles = (a.m.N + 2 * kCh - 1) / (2 * kCh) * ((a.m.T + BT - 1) / BT);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * std::min(tiles, sm_count() / 2));
-    cfg.blockDim = dim3(kPairThr);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = a.chained ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, q8_pair_kernel, a, wmap, xmap);
+    return launch_ordered(q8_pair_kernel, 2 * std::min(tiles, sm_count() / 2), kPairThr, C::kSmem, s, a, wmap, xmap);
 }
 
 }  // namespace

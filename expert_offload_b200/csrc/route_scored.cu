@@ -24,6 +24,7 @@
 #include <cfloat>
 
 #include "device.cuh"
+#include "launch.cuh"
 
 namespace hfq {
 namespace {
@@ -554,10 +555,11 @@ __device__ __forceinline__ void route_token(const Args &a, int t, int lane, bool
 
 // Without lists: warps walk the tokens.
 template <int N>
-__global__ void __launch_bounds__(256, N > 16 ? 1 : 3) route_scored_kernel(const Args a)
+__global__ void __launch_bounds__(256, N > 16 ? 1 : 3) route_scored_kernel(Args a)
 {
     __shared__ Cand cand[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    begin_ordered();
     float w;
     int e;
     const bool masks = bias_masks(a, lane);
@@ -630,12 +632,12 @@ __device__ __forceinline__ int exclusive_sum(int v, int *wsum)
 
 // With lists, several chunks: a block routes a.tok tokens and counts its pairs.
 template <int N>
-__global__ void __launch_bounds__(kListWarps * 32, N > 16 ? 1 : 4) route_count_kernel(const Args a)
+__global__ void __launch_bounds__(kListWarps * 32, N > 16 ? 1 : 4) route_count_kernel(Args a)
 {
     __shared__ Cand cand[kListWarps];
     __shared__ int count[HFQ_MAX_EXPERTS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    begin_ordered();
     for (int i = tid; i < a.E; i += kListWarps * 32) count[i] = 0;
     float w;
     int e;
@@ -653,7 +655,7 @@ __global__ void __launch_bounds__(kListWarps * 32, N > 16 ? 1 : 4) route_count_k
 // With lists, up to 16 tokens: one block routes them, a warp each, and writes
 // the lists.
 template <int N>
-__global__ void __launch_bounds__(kPlaceThr) route_alone_kernel(const Args a)
+__global__ void __launch_bounds__(kPlaceThr) route_alone_kernel(Args a)
 {
     __shared__ Cand cand[kPlaceWarps];
     __shared__ __align__(16) Placer place;
@@ -661,6 +663,7 @@ __global__ void __launch_bounds__(kPlaceThr) route_alone_kernel(const Args a)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     float w;
     int e;
+    begin_ordered();
     const bool masks = bias_masks(a, lane);
     clear_counts(place);
     place.start[tid] = 0;
@@ -685,10 +688,10 @@ __global__ void __launch_bounds__(kPlaceThr) route_alone_kernel(const Args a)
 
 // Adds up the counts of many chunks, expert by expert, a warp each: base[c][e]
 // becomes the pairs of e in the chunks before c, cnt[e] the total.
-__global__ void lists_scan_kernel(const uint16_t *__restrict__ hist, int chunks, int E, int32_t *__restrict__ base,
-                                  int32_t *__restrict__ cnt)
+__global__ void lists_scan_kernel(const uint16_t *hist, int chunks, int E, int32_t *base, int32_t *cnt)
 {
     const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    begin_ordered();
     if (e >= E) return;
     int sum = 0;
     for (int c0 = 0; c0 < chunks; c0 += 32) {
@@ -711,9 +714,8 @@ __global__ void lists_scan_kernel(const uint16_t *__restrict__ hist, int chunks,
 // counts, 256 x 512 x 2 bytes at most, instead of a kernel between.
 static_assert(kScanChunks * kTokMax < 65536, "sums of the counts fit 16 bits");
 __global__ void __launch_bounds__(kPlaceThr)
-lists_place_kernel(const int32_t *idx, const uint16_t *hist, const int32_t *__restrict__ base,
-                   int chunks, int group, int P, int per_chunk, int E, int32_t *__restrict__ cnt,
-                   int32_t *__restrict__ off, int32_t *__restrict__ perm)
+lists_place_kernel(const int32_t *idx, const uint16_t *hist, const int32_t *base, int chunks, int group, int P,
+                   int per_chunk, int E, int32_t *cnt, int32_t *off, int32_t *perm)
 {
     __shared__ __align__(16) Placer s;
     __shared__ int wsum[kPlaceWarps], total_of[HFQ_MAX_EXPERTS], before_of[HFQ_MAX_EXPERTS];
@@ -722,7 +724,7 @@ lists_place_kernel(const int32_t *idx, const uint16_t *hist, const int32_t *__re
     total_of[tid] = before_of[tid] = 0;
     clear_counts(s);
     __syncthreads();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    begin_ordered();
     if (base) {
         if (tid < E) before_of[tid] = base[(size_t)first * E + tid], total_of[tid] = cnt[tid];
     } else {
@@ -873,47 +875,32 @@ hfq_status moe_route_scored(const void *logits, hfq_dtype logits_dtype, int ld, 
     a.vec = aligned16(logits) && a.ld % unit == 0 && a.size % unit == 0 && a.run % unit == 0 && a.size % a.run == 0;
     a.bias_vec = aligned16(bias) && a.size % 4 == 0 && a.run % 4 == 0 && a.size % a.run == 0;
     cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t err;
     if (!lists) {
         // a warp a token up to one block an SM, then blocks of up to eight warps,
         // which walk the tokens once there are more than eight blocks an SM
         const int sms = std::max(1, sm_count());
         const int warps = T <= sms ? 1 : T <= 4 * sms ? 4 : 8;
         const int grid = std::min((T + warps - 1) / warps, 8 * sms);
-        if (a.run <= 8) route_scored_kernel<8><<<grid, warps * 32, 0, s>>>(a);
-        else if (a.run <= 16) route_scored_kernel<16><<<grid, warps * 32, 0, s>>>(a);
-        else route_scored_kernel<32><<<grid, warps * 32, 0, s>>>(a);
+        void (*kernel)(Args) = a.run <= 8 ? route_scored_kernel<8> : a.run <= 16 ? route_scored_kernel<16> : route_scored_kernel<32>;
+        err = launch_ordered(kernel, grid, warps * 32, 0, s, a);
+    } else if (!need) {
+        void (*kernel)(Args) = a.run <= 8 ? route_alone_kernel<8> : a.run <= 16 ? route_alone_kernel<16> : route_alone_kernel<32>;
+        err = launch_ordered(kernel, 1, kPlaceThr, 0, s, a);
     } else {
-        const int chunks = (T + a.tok - 1) / a.tok, thr = kListWarps * 32;
-        if (!need) {
-            if (a.run <= 8) route_alone_kernel<8><<<1, kPlaceThr, 0, s>>>(a);
-            else if (a.run <= 16) route_alone_kernel<16><<<1, kPlaceThr, 0, s>>>(a);
-            else route_alone_kernel<32><<<1, kPlaceThr, 0, s>>>(a);
-        } else {
-            if (a.run <= 8) route_count_kernel<8><<<chunks, thr, 0, s>>>(a);
-            else if (a.run <= 16) route_count_kernel<16><<<chunks, thr, 0, s>>>(a);
-            else route_count_kernel<32><<<chunks, thr, 0, s>>>(a);
-            int32_t *base = nullptr;
-            int group = std::max(1, kPlaceThr / (a.tok * k));       // one pass of a placing block
-            if (chunks > kScanChunks) {
-                base = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + round256((size_t)chunks * E * 2));
-                lists_scan_kernel<<<(E + 7) / 8, 256, 0, s>>>(a.hist, chunks, E, base, cnt);
-            }
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3((chunks + group - 1) / group);
-            cfg.blockDim = dim3(kPlaceThr);
-            cfg.stream = s;
-            cudaLaunchAttribute attr;
-            attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-            attr.val.programmaticStreamSerializationAllowed = 1;
-            cfg.attrs = &attr;
-            cfg.numAttrs = base ? 0 : 1;           // behind the counting kernel it may start early
-            const cudaError_t e = cudaLaunchKernelEx(&cfg, lists_place_kernel, (const int32_t *)idx,
-                                                     (const uint16_t *)a.hist, (const int32_t *)base, chunks, group,
-                                                     T * k, a.tok * k, E, cnt, off, perm);
-            if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "moe_route_scored launch: %s", cudaGetErrorString(e));
+        const int chunks = (T + a.tok - 1) / a.tok;
+        const int group = std::max(1, kPlaceThr / (a.tok * k));     // one pass of a placing block
+        void (*kernel)(Args) = a.run <= 8 ? route_count_kernel<8> : a.run <= 16 ? route_count_kernel<16> : route_count_kernel<32>;
+        err = launch_ordered(kernel, chunks, kListWarps * 32, 0, s, a);
+        int32_t *base = nullptr;
+        if (chunks > kScanChunks) {
+            base = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + round256((size_t)chunks * E * 2));
+            if (err == cudaSuccess) err = launch_ordered(lists_scan_kernel, (E + 7) / 8, 256, 0, s, a.hist, chunks, E, base, cnt);
         }
+        if (err == cudaSuccess)
+            err = launch_ordered(lists_place_kernel, (chunks + group - 1) / group, kPlaceThr, 0, s, idx, a.hist, base, chunks,
+                                 group, T * k, a.tok * k, E, cnt, off, perm);
     }
-    const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return fail(HFQ_ERR_CUDA, "moe_route_scored launch: %s", cudaGetErrorString(err));
     return ok();
 }
