@@ -23,8 +23,8 @@
 #include <algorithm>
 #include <cfloat>
 
-#include "device.cuh"
 #include "launch.cuh"
+#include "quant8.cuh"
 
 namespace hfq {
 namespace {
@@ -40,7 +40,7 @@ struct Args {
     const float *bias;
     int32_t *idx;
     float *wts;
-    uint16_t *hist;              // [chunks][E], or null without the lists
+    uint8_t *hist;               // [chunks][round16(E)], or null without several chunks
     int32_t *cnt, *off, *perm;   // one block alone: it writes the lists itself
     size_t ld;
     int T, E, k;
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(kListWarps * 32, N > 16 ? 1 : 4) route_count_k
     __shared__ int count[HFQ_MAX_EXPERTS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     begin_ordered();
-    for (int i = tid; i < a.E; i += kListWarps * 32) count[i] = 0;
+    for (int i = tid; i < HFQ_MAX_EXPERTS; i += kListWarps * 32) count[i] = 0;
     float w;
     int e;
     const bool masks = bias_masks(a, lane);
@@ -649,7 +649,11 @@ __global__ void __launch_bounds__(kListWarps * 32, N > 16 ? 1 : 4) route_count_k
         if (lane < a.k) atomicAdd(&count[e], 1);
     }
     __syncthreads();
-    for (int i = tid; i < a.E; i += kListWarps * 32) a.hist[(size_t)blockIdx.x * a.E + i] = (uint16_t)count[i];
+    // a chunk sends an expert at most one pair a token: a byte holds the count
+    const int stride = (int)round16(a.E);
+    for (int i = 4 * tid; i < stride; i += 4 * kListWarps * 32)
+        *reinterpret_cast<uint32_t *>(a.hist + (size_t)blockIdx.x * stride + i) =
+            (uint32_t)count[i] | (uint32_t)count[i + 1] << 8 | (uint32_t)count[i + 2] << 16 | (uint32_t)count[i + 3] << 24;
 }
 
 // With lists, up to 16 tokens: one block routes them, a warp each, and writes
@@ -688,7 +692,7 @@ __global__ void __launch_bounds__(kPlaceThr) route_alone_kernel(Args a)
 
 // Adds up the counts of many chunks, expert by expert, a warp each: base[c][e]
 // becomes the pairs of e in the chunks before c, cnt[e] the total.
-__global__ void lists_scan_kernel(const uint16_t *hist, int chunks, int E, int32_t *base, int32_t *cnt)
+__global__ void lists_scan_kernel(const uint8_t *hist, int chunks, int E, int32_t *base, int32_t *cnt)
 {
     const int e = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     begin_ordered();
@@ -696,7 +700,7 @@ __global__ void lists_scan_kernel(const uint16_t *hist, int chunks, int E, int32
     int sum = 0;
     for (int c0 = 0; c0 < chunks; c0 += 32) {
         const int c = c0 + lane;
-        const int v = c < chunks ? hist[(size_t)c * E + e] : 0;
+        const int v = c < chunks ? hist[(size_t)c * round16(E) + e] : 0;
         int s = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -711,72 +715,63 @@ __global__ void lists_scan_kernel(const uint16_t *hist, int chunks, int E, int32
 
 // Places the pairs of `group` consecutive chunks.  The counts of the chunks
 // before come from base, or (base null) are added up here: all blocks read all
-// counts, 256 x 512 x 2 bytes at most, instead of a kernel between.
-static_assert(kScanChunks * kTokMax < 65536, "sums of the counts fit 16 bits");
+// counts, 256 x 512 bytes at most, instead of a kernel between.
+static_assert(kTokMax < 256 && kScanChunks * kTokMax < 65536, "a count fits 8 bits, sums of counts 16");
 __global__ void __launch_bounds__(kPlaceThr)
-lists_place_kernel(const int32_t *idx, const uint16_t *hist, const int32_t *base, int chunks, int group, int P,
+lists_place_kernel(const int32_t *idx, const uint8_t *hist, const int32_t *base, int chunks, int group, int P,
                    int per_chunk, int E, int32_t *cnt, int32_t *off, int32_t *perm)
 {
     __shared__ __align__(16) Placer s;
-    __shared__ int wsum[kPlaceWarps], total_of[HFQ_MAX_EXPERTS], before_of[HFQ_MAX_EXPERTS];
+    __shared__ int wsum[kPlaceWarps];
+    // sums of experts 16 x + 4 j + i and 16 x + 4 j + i + 2 in the halves of word [j][i][x]
+    __shared__ uint32_t total_of[4][2][32], before_of[4][2][32];
     const int tid = threadIdx.x;
     const int first = blockIdx.x * group;
-    total_of[tid] = before_of[tid] = 0;
+    if (tid < 256) total_of[0][0][tid] = before_of[0][0][tid] = 0;
     clear_counts(s);
     __syncthreads();
     begin_ordered();
+    int total = 0, before = 0;
     if (base) {
-        if (tid < E) before_of[tid] = base[(size_t)first * E + tid], total_of[tid] = cnt[tid];
+        if (tid < E) before = base[(size_t)first * E + tid], total = cnt[tid];
     } else {
-        // Sums of all chunks' counts fit 16 bits (kScanChunks * kTokMax tokens), so
-        // two neighbours are added as one word: a thread takes eight experts of
-        // every kPlaceThr / (E / 8)-th chunk, many in flight.
-        constexpr int kU = 16;
-        if (E % 8 == 0) {
-            const int lanes = E / 8, rows = kPlaceThr / lanes, x = tid % lanes, r0 = tid / lanes;
-            uint4 t = make_uint4(0u, 0u, 0u, 0u), b = t;
-            if (r0 < rows) {
-                for (int c0 = r0; c0 < chunks; c0 += kU * rows) {
-                    uint4 v[kU];
+        // a thread takes 16 experts of every kRows-th chunk, all its loads in flight
+        constexpr int kRows = kPlaceThr / 32, kU = kScanChunks / kRows;
+        const int x = tid & 31, r0 = tid >> 5, stride = (int)round16(E);
+        if (16 * x < stride) {
+            uint4 v[kU];
 #pragma unroll
-                    for (int i = 0; i < kU; ++i)
-                        v[i] = c0 + i * rows < chunks
-                                   ? *reinterpret_cast<const uint4 *>(hist + (size_t)(c0 + i * rows) * E + 8 * x)
-                                   : make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < kU; ++i)
+                v[i] = r0 + i * kRows < chunks
+                           ? *reinterpret_cast<const uint4 *>(hist + (size_t)(r0 + i * kRows) * stride + 16 * x)
+                           : make_uint4(0u, 0u, 0u, 0u);
+            uint32_t t[8] = {0, 0, 0, 0, 0, 0, 0, 0}, b[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
-                    for (int i = 0; i < kU; ++i) {
-                        t.x += v[i].x, t.y += v[i].y, t.z += v[i].z, t.w += v[i].w;
-                        if (c0 + i * rows < first) b.x += v[i].x, b.y += v[i].y, b.z += v[i].z, b.w += v[i].w;
-                    }
-                }
-                const uint32_t tw[4] = {t.x, t.y, t.z, t.w}, bw[4] = {b.x, b.y, b.z, b.w};
+            for (int i = 0; i < kU; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                const bool early = r0 + i * kRows < first;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    atomicAdd(&total_of[8 * x + 2 * i], (int)(tw[i] & 0xffffu));
-                    atomicAdd(&total_of[8 * x + 2 * i + 1], (int)(tw[i] >> 16));
-                    atomicAdd(&before_of[8 * x + 2 * i], (int)(bw[i] & 0xffffu));
-                    atomicAdd(&before_of[8 * x + 2 * i + 1], (int)(bw[i] >> 16));
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t even = w[j] & 0x00ff00ffu, odd = w[j] >> 8 & 0x00ff00ffu;
+                    t[2 * j] += even, t[2 * j + 1] += odd;
+                    if (early) b[2 * j] += even, b[2 * j + 1] += odd;
                 }
             }
-        } else if (tid < E) {
-            int t = 0, b = 0;
-            for (int c0 = 0; c0 < chunks; c0 += kU) {
-                int v[kU];
 #pragma unroll
-                for (int i = 0; i < kU; ++i) v[i] = c0 + i < chunks ? hist[(size_t)(c0 + i) * E + tid] : 0;
-#pragma unroll
-                for (int i = 0; i < kU; ++i) {
-                    t += v[i];
-                    if (c0 + i < first) b += v[i];
-                }
+            for (int j = 0; j < 8; ++j) {
+                atomicAdd(&total_of[j / 2][j & 1][x], t[j]);
+                atomicAdd(&before_of[j / 2][j & 1][x], b[j]);
             }
-            total_of[tid] = t;
-            before_of[tid] = b;
+        }
+        __syncthreads();
+        if (tid < E) {
+            const int j = tid >> 2 & 3, i = tid & 1, up = tid >> 1 & 1;
+            total = (int)(total_of[j][i][tid >> 4] >> 16 * up & 0xffffu);
+            before = (int)(before_of[j][i][tid >> 4] >> 16 * up & 0xffffu);
         }
     }
-    __syncthreads();
-    const int total = total_of[tid], sum = exclusive_sum(total, wsum);
-    s.start[tid] = sum + before_of[tid];
+    const int sum = exclusive_sum(total, wsum);
+    s.start[tid] = sum + before;
     if (blockIdx.x == 0 && tid < E) {
         off[tid] = sum;
         if (!base) cnt[tid] = total;
@@ -817,7 +812,7 @@ size_t moe_route_scored_workspace_bytes(int T, int E, int k)
 {
     if (T < 1 || E < 1 || k < 1 || T <= kAlone) return 0;
     const size_t chunks = ((size_t)T + chunk_tokens(T) - 1) / chunk_tokens(T);
-    return round256(chunks * E * sizeof(uint16_t)) + (chunks > kScanChunks ? chunks * E * sizeof(int32_t) : 0);
+    return round256(chunks * round16((size_t)E)) + (chunks > kScanChunks ? chunks * E * sizeof(int32_t) : 0);
 }
 
 hfq_status moe_route_scored(const void *logits, hfq_dtype logits_dtype, int ld, int T, int E,
@@ -862,7 +857,7 @@ hfq_status moe_route_scored(const void *logits, hfq_dtype logits_dtype, int ld, 
 
     Args a;
     a.logits = logits; a.bias = bias; a.idx = idx; a.wts = wts;
-    a.hist = lists && need ? static_cast<uint16_t *>(workspace) : nullptr;
+    a.hist = lists && need ? static_cast<uint8_t *>(workspace) : nullptr;
     a.cnt = cnt; a.off = off; a.perm = perm;
     a.ld = ld ? ld : E; a.T = T; a.E = E; a.k = k;
     a.n_groups = n; a.size = E / n; a.topk_groups = rule->topk_groups; a.group_top = rule->group_top;
@@ -894,7 +889,7 @@ hfq_status moe_route_scored(const void *logits, hfq_dtype logits_dtype, int ld, 
         err = launch_ordered(kernel, chunks, kListWarps * 32, 0, s, a);
         int32_t *base = nullptr;
         if (chunks > kScanChunks) {
-            base = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + round256((size_t)chunks * E * 2));
+            base = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + round256((size_t)chunks * round16(E)));
             if (err == cudaSuccess) err = launch_ordered(lists_scan_kernel, (E + 7) / 8, 256, 0, s, a.hist, chunks, E, base, cnt);
         }
         if (err == cudaSuccess)
