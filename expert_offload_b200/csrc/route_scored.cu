@@ -478,11 +478,10 @@ __device__ __forceinline__ void read_bias(const Args &a, int e0, int n, float (&
     }
 }
 
-// The lane's logits, masked ones -inf.
+// The lane's logits as they are (-inf behind its run).
 
 template <int N>
-__device__ __forceinline__ void read_logits(const Args &a, size_t row, int e0, int n, const float (&b)[N], bool masks,
-                                            float (&l)[N])
+__device__ __forceinline__ void load_logits(const Args &a, size_t row, int e0, int n, float (&l)[N])
 {
     if (a.vec) {                 // whole 16-byte pieces
         if (a.bf16) {
@@ -510,6 +509,12 @@ __device__ __forceinline__ void read_logits(const Args &a, size_t row, int e0, i
                    : a.bf16  ? bf16_bits_to_float(static_cast<const uint16_t *>(a.logits)[row + e0 + i])
                              : static_cast<const float *>(a.logits)[row + e0 + i];
     }
+}
+
+// The rule's reading of them: masked ones -inf.
+template <int N>
+__device__ __forceinline__ void read_logits(int n, const float (&b)[N], bool masks, float (&l)[N])
+{
     const float least = n > 0 ? -FLT_MAX : INFINITY;     // a lane without experts has none
 #pragma unroll
     for (int i = 0; i < N; ++i) l[i] = l[i] >= least ? fminf(l[i], FLT_MAX) : -INFINITY;
@@ -522,16 +527,16 @@ __device__ __forceinline__ void read_logits(const Args &a, size_t row, int e0, i
 
 // The whole of one token; lane j < k ends with its slot j.
 template <int N>
-__device__ __forceinline__ void route_token(const Args &a, int t, int lane, bool masks, Cand &cand, int &e,
-                                            float &w)
+__device__ __forceinline__ void route_token(const Args &a, int t, int lane, bool masks, float (&l)[N],
+                                            Cand &cand, int &e, float &w)
 {
     const int grp = lane / a.tpl, part = lane - grp * a.tpl;
     const int e0 = grp * a.size + part * a.run;
     const int n = grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0;
     const size_t row = (size_t)t * a.ld;
-    float l[N], b[N];
+    float b[N];
     read_bias(a, e0, n, b);
-    read_logits(a, row, e0, n, b, masks, l);
+    read_logits(n, b, masks, l);
     float m = 0.0f, z = 1.0f;
     if (!a.sigmoid && (a.bias || !a.renorm || a.group_top > 1)) {
         m = -INFINITY;
@@ -553,17 +558,49 @@ __device__ __forceinline__ void route_token(const Args &a, int t, int lane, bool
     }
 }
 
+// The logits of token t for this lane.
+template <int N>
+__device__ __forceinline__ void fetch(const Args &a, int t, int lane, float (&l)[N])
+{
+    const int grp = lane / a.tpl, part = lane - grp * a.tpl;
+    load_logits(a, (size_t)t * a.ld, grp * a.size + part * a.run,
+                grp < a.n_groups ? min(a.run, a.size - part * a.run) : 0, l);
+}
+
+// Tokens t, t + step, ... below end, by one warp: the next token's logits are
+// requested before the current one is decided.
+template <int N, class Done>
+__device__ __forceinline__ void route_tokens(const Args &a, int t, int step, int end, int lane, bool masks, Cand &cand,
+                                             Done done)
+{
+    float next[N];
+    if (t < end) fetch(a, t, lane, next);
+    for (; t < end; t += step) {
+        float l[N], w;
+        int e;
+#pragma unroll
+        for (int i = 0; i < N; ++i) l[i] = next[i];
+        if (t + step < end) fetch(a, t + step, lane, next);
+        route_token<N>(a, t, lane, masks, l, cand, e, w);
+        done(e);
+    }
+}
+
+// Blocks of eight warps that an SM holds.  With more of them there would be more
+// tokens at once, but the next token's logits in registers are worth more: 8192
+// tokens of 512 experts take 14.3 us with two blocks, 16.4 with three and 18.6
+// with four (whose registers spill); of 256 experts 14.3, 12.7 and 15.0.
+constexpr int blocks_of(int run) { return run > 16 ? 1 : run > 8 ? 2 : 3; }
+
 // Without lists: warps walk the tokens.
 template <int N>
-__global__ void __launch_bounds__(256, N > 16 ? 1 : 3) route_scored_kernel(Args a)
+__global__ void __launch_bounds__(256, blocks_of(N)) route_scored_kernel(Args a)
 {
     __shared__ Cand cand[8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     begin_ordered();
-    float w;
-    int e;
     const bool masks = bias_masks(a, lane);
-    for (int t = blockIdx.x * warps + warp; t < a.T; t += gridDim.x * warps) route_token<N>(a, t, lane, masks, cand[warp], e, w);
+    route_tokens<N>(a, blockIdx.x * warps + warp, gridDim.x * warps, a.T, lane, masks, cand[warp], [](int) {});
 }
 
 // ------------------------------------------------------------ the pair lists
@@ -632,22 +669,19 @@ __device__ __forceinline__ int exclusive_sum(int v, int *wsum)
 
 // With lists, several chunks: a block routes a.tok tokens and counts its pairs.
 template <int N>
-__global__ void __launch_bounds__(kListWarps * 32, N > 16 ? 1 : 4) route_count_kernel(Args a)
+__global__ void __launch_bounds__(kListWarps * 32, N > 16 ? 1 : 2) route_count_kernel(Args a)
 {
     __shared__ Cand cand[kListWarps];
     __shared__ int count[HFQ_MAX_EXPERTS];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     begin_ordered();
     for (int i = tid; i < HFQ_MAX_EXPERTS; i += kListWarps * 32) count[i] = 0;
-    float w;
-    int e;
     const bool masks = bias_masks(a, lane);
     __syncthreads();
     const int t_end = min(a.T, ((int)blockIdx.x + 1) * a.tok);
-    for (int t = blockIdx.x * a.tok + warp; t < t_end; t += kListWarps) {
-        route_token<N>(a, t, lane, masks, cand[warp], e, w);
+    route_tokens<N>(a, blockIdx.x * a.tok + warp, kListWarps, t_end, lane, masks, cand[warp], [&](int e) {
         if (lane < a.k) atomicAdd(&count[e], 1);
-    }
+    });
     __syncthreads();
     // a chunk sends an expert at most one pair a token: a byte holds the count
     const int stride = (int)round16(a.E);
@@ -665,20 +699,17 @@ __global__ void __launch_bounds__(kPlaceThr) route_alone_kernel(Args a)
     __shared__ __align__(16) Placer place;
     __shared__ int wsum[kPlaceWarps], sel[kPlaceWarps * HFQ_MAX_TOPK];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    float w;
-    int e;
     begin_ordered();
     const bool masks = bias_masks(a, lane);
     clear_counts(place);
     place.start[tid] = 0;
     __syncthreads();
-    if (warp < a.T) {
-        route_token<N>(a, warp, lane, masks, cand[warp], e, w);
+    route_tokens<N>(a, warp, kPlaceWarps, a.T, lane, masks, cand[warp], [&](int e) {
         if (lane < a.k) {
             sel[warp * a.k + lane] = e;
             atomicAdd(&place.start[e], 1);
         }
-    }
+    });
     __syncthreads();
     const int total = place.start[tid], sum = exclusive_sum(total, wsum);
     place.start[tid] = sum;
@@ -731,6 +762,8 @@ lists_place_kernel(const int32_t *idx, const uint8_t *hist, const int32_t *base,
     clear_counts(s);
     __syncthreads();
     begin_ordered();
+    const int q0 = first * per_chunk, p1 = min(P, (first + group) * per_chunk);
+    const int e0 = q0 + tid < p1 ? idx[q0 + tid] : -1;       // the first pass' pairs, needed last
     int total = 0, before = 0;
     if (base) {
         if (tid < E) before = base[(size_t)first * E + tid], total = cnt[tid];
@@ -777,11 +810,10 @@ lists_place_kernel(const int32_t *idx, const uint8_t *hist, const int32_t *base,
         if (!base) cnt[tid] = total;
         if (tid == E - 1) off[E] = sum + total;
     }
-    const int p1 = min(P, (first + group) * per_chunk);
-    for (int p0 = first * per_chunk; p0 < p1; p0 += kPlaceThr) {
-        const int p = p0 + tid;
-        if (p0 > first * per_chunk) next_pairs(s, E);
-        place_pairs(s, p < p1 ? idx[p] : -1, p, perm);
+    place_pairs(s, e0, q0 + tid, perm);
+    for (int p0 = q0 + kPlaceThr; p0 < p1; p0 += kPlaceThr) {
+        next_pairs(s, E);
+        place_pairs(s, p0 + tid < p1 ? idx[p0 + tid] : -1, p0 + tid, perm);
     }
 }
 
@@ -872,11 +904,11 @@ hfq_status moe_route_scored(const void *logits, hfq_dtype logits_dtype, int ld, 
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t err;
     if (!lists) {
-        // a warp a token up to one block an SM, then blocks of up to eight warps,
-        // which walk the tokens once there are more than eight blocks an SM
+        // a warp a token up to one block an SM, then blocks of up to eight warps, as
+        // many as SMs hold, which walk the tokens
         const int sms = std::max(1, sm_count());
         const int warps = T <= sms ? 1 : T <= 4 * sms ? 4 : 8;
-        const int grid = std::min((T + warps - 1) / warps, 8 * sms);
+        const int grid = std::min((T + warps - 1) / warps, blocks_of(a.run) * sms);
         void (*kernel)(Args) = a.run <= 8 ? route_scored_kernel<8> : a.run <= 16 ? route_scored_kernel<16> : route_scored_kernel<32>;
         err = launch_ordered(kernel, grid, warps * 32, 0, s, a);
     } else if (!need) {
