@@ -187,8 +187,9 @@ struct Reds {
         return __reduce_max_sync(0xffffffffu, __float_as_uint(red[which][lane & (kMaxWarps - 1)]));
     }
 
-    // 1 / sqrt(mean(v^2) + eps).  Where the sum of squares leaves the f32 range
-    // the row is scaled by 2^-64 (in v, too) and summed again.
+    // 1 / sqrt(mean(v^2) + eps).  Where squares leave the f32 range (above, or
+    // below with an eps that does not cover it) the row is scaled, in v, too, and
+    // summed again.
     template <int NV>
     __device__ __forceinline__ float inv_rms(int which, float (&v)[NV][8], float inv_h, float eps) const
     {
@@ -198,17 +199,19 @@ struct Reds {
 #pragma unroll
             for (int i = 0; i < 8; ++i) s = fmaf(v[c][i], v[c][i], s);
         s = sum(which, s);
-        if (!(s <= FLT_MAX)) {
+        const bool small = s < 0x1p-60f && eps < 0x1p-60f;
+        if (!(s <= FLT_MAX) || small) {
+            const float f = small ? 0x1p64f : 0x1p-80f;
             s = 0.0f;
 #pragma unroll
             for (int c = 0; c < NV; ++c)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    v[c][i] *= 0x1p-64f;
+                    v[c][i] *= f;
                     s = fmaf(v[c][i], v[c][i], s);
                 }
             s = sum(which + 1, s);
-            eps *= 0x1p-128f;
+            eps = eps * f * f;
         }
         float r;
         asm("rsqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(fmaf(s, inv_h, eps)));       // within 2^-22.9
@@ -421,7 +424,7 @@ extern "C" hfq_status moe_norm_residual(const moe_norm_rule *rule, int T, int H,
     a.y2_gate = y2_gate; a.gate = gate; a.x_out = x_out; a.xn = xn; a.xq = xq; a.xq_scale = xq_scale;
     a.ldx = ldx ? ldx : H; a.ldy = ldy ? ldy : H; a.T = T; a.H = H;
     a.w_bf16 = rule->w_dtype == HFQ_BF16; a.xn_bf16 = xn_dtype == HFQ_BF16;
-    a.gate_kind = rule->gate_kind; a.gate_sigmoid = rule->gate_act == HFQ_GATE_SIGMOID;
+    a.gate_kind = y ? rule->gate_kind : HFQ_GATE_NONE; a.gate_sigmoid = rule->gate_act == HFQ_GATE_SIGMOID;
     a.inv_h = 1.0f / (float)H;
     a.eps = rule->eps; a.w_offset = rule->w_offset; a.alpha = rule->residual_scale; a.beta = rule->branch_scale;
 

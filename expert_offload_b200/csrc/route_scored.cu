@@ -313,13 +313,13 @@ __device__ __forceinline__ Slot select_token(const Args &a, size_t row, const fl
     const int grp = lane / a.tpl, part = lane - grp * a.tpl;
     const int e0 = grp * a.size + part * a.run;
     const bool scored = a.bias || (a.n_groups > 1 && a.group_top > 1);
-    // Errors, in units of 2^-24.  Sigmoid: the exponential is off by 4 and by 1.5
-    // for each unit of |l| (the product's and the constant's rounding), which a
-    // score of at most 1 / (1 + exp(|l|)) turns into less than 0.5; sum 1,
-    // reciprocal 2: under 8.  Softmax: the same for numerator and sum, 21
-    // additions of the sum, quotient 2: under 33 of the largest score 1 / z.  The
-    // bias' addition: |c|.
-    const float smax = a.sigmoid ? 1.0f : rcp_approx(z), base = kU * (a.sigmoid ? 8.0f : 36.0f * smax);
+    // Errors, in units of 2^-24.  An exponential is off by 4, and by 1.5 for each
+    // unit of its argument (rounding of the product, of the constant).  Sigmoid:
+    // that counts s (1 - s) times, under 1.4 in all; sum 1, reciprocal 2: under 8.
+    // Softmax: numerator 4 (far ones are small), sum 4 + 1.5 times the mean
+    // distance (at most ln 512) + 35 additions, quotient 3: under 64 of the
+    // largest score, 1 / z.  The bias' addition: |c|.
+    const float smax = a.sigmoid ? 1.0f : rcp_approx(z), base = kU * (a.sigmoid ? 8.0f : 64.0f * smax);
     float c[N];                  // what experts are compared by
     bool keep = grp < a.n_groups;
     if (scored) {

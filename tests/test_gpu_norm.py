@@ -202,6 +202,24 @@ def test_rows_whose_squares_leave_the_f32_range(eo):
     c.call().check()
 
 
+@pytest.mark.parametrize("H", [64, 1000, 1001, 8192])
+def test_rows_at_the_ends_of_the_f32_range(eo, H):
+    """Rows up to the largest f32, and rows whose squares underflow where no eps covers them."""
+    for scale, eps in ((1.0, 1e-6), (2.0 ** -100, 0.0), (2.0 ** -70, 0.0), (2.0 ** -30, 2.0 ** -62)):
+        c = Case(eo, 3, H, "f32", "f32", branch=False, eps=eps)
+        c.x.copy_(c.x / c.x.abs().max() * (3.4e38 if scale == 1.0 else 1.0) * scale)
+        c.x0 = c.x.clone()
+        c.call().check()
+
+
+def test_a_rule_with_a_gate_serves_a_row_without_a_block(eo):
+    """A gate's kind says nothing where there is no block: the plain norm."""
+    for gate in ("token", "channel", "full"):
+        c = Case(eo, 7, 256, branch=False)
+        c.kind = ("none", "token", "channel", "full").index(gate)
+        c.call().check()
+
+
 def test_nan_and_infinity_stay_in_their_row(eo):
     for H in (256, 1001):
         a = Case(eo, 6, H, "bf16", "f32", shared="gate", quant=True, seed=1)

@@ -283,22 +283,29 @@ def test_offsets_past_32_bits(eo):
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(eo):
     """The test hook makes the tensor-core kernel wait for an arrival that never
     comes; the wait is bounded, the status says so once."""
-    T, K, N = 40, 1024, 300
-    xq, xs = torch.ones(T, K, dtype=torch.int8, device="cuda"), torch.ones(T, device="cuda")
-    w, ws = _weights(1, N, K, K)
-    y = torch.empty(T, N, device="cuda")
     eo.hfq_set_option(eo.OPT_WAIT_TIMEOUT_NS, 2_000_000)
     try:
-        for split_k in (K, 128):                         # a cluster, and one CTA alone
+        for T, K, N in ((40, 1024, 300), (40, 128, 300), (5, 1024, 300), (1024, 256, 4096)):
+            # a cluster, one CTA alone, the fused kernel, CTA pairs
+            x = torch.randint(-9, 10, (T, K), device="cuda").float()
+            x[:, 0] = 127.0                              # scale 1: the values are the integers
+            q, one = x.to(torch.int8), torch.ones(T, device="cuda")
+            w, ws = _weights(1, N, K, K)
+            y = torch.empty(T, N, device="cuda")
+            work = torch.zeros(eo.q8_linear_workspace_bytes(T, K, N) or 1, dtype=torch.uint8, device="cuda")
+
+            def call():
+                eo.q8_linear(x, eo.HFQ_F32, T, K, w, ws, N, y, eo.HFQ_F32, work)
+
             eo.hfq_set_option(eo.OPT_TEST_MISSING_ARRIVALS, 1)
-            eo.q8_matmul(xq, xs, T, split_k, w, ws, N, y, eo.HFQ_F32, ldxq=K, ldw=K)
+            call()
             with pytest.raises(eo.HfqError) as e:
                 eo.hfq_workspace_status(None)
             assert e.value.status == -6
             eo.hfq_workspace_status(None)
-            eo.q8_matmul(xq, xs, T, split_k, w, ws, N, y, eo.HFQ_F32, ldxq=K, ldw=K)
+            call()
             eo.hfq_workspace_status(None)
-            _close(y, _exact(xq, xs, w, ws, split_k), "f32")
+            _close(y, _exact(q, one, w, ws, K), "f32")
     finally:
         eo.hfq_set_option(eo.OPT_WAIT_TIMEOUT_NS, 1_000_000_000)
         eo.hfq_set_option(eo.OPT_TEST_MISSING_ARRIVALS, 0)
