@@ -38,7 +38,7 @@ struct Args {
 __device__ __forceinline__ float sigmoid(float v)
 {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-v)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-v)));
     return r;
 }
 
@@ -97,10 +97,23 @@ struct Row {
         }
     }
 
-    __device__ __forceinline__ void load_as(const void *p, size_t base, bool bf16, uint32_t (&w)[NV][8]) const
+    // A row of weights as floats.
+    __device__ __forceinline__ void load_weights(const void *p, bool bf16, float (&v)[NV][8]) const
     {
-        if (bf16) load<true>(p, base, w);
-        else load<false>(p, base, w);
+        uint32_t w[NV][8];
+        if (bf16) {
+            load<true>(p, 0, w);
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[c][i] = value<true>(w[c], i);
+        } else {
+            load<false>(p, 0, w);
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[c][i] = __uint_as_float(w[c][i]);
+        }
     }
 
     template <bool BF16>
@@ -158,15 +171,22 @@ constexpr int kReds = 5;
 constexpr int kMaxWarps = 16;
 
 struct Reds {
-    float (*red)[kMaxWarps];              // [kReds] of this row; words of absent warps are 0
+    float (*red)[kMaxWarps];              // [kReds]
     int nt;
+
+    // This warp's word; the words of absent warps are 0.
+    __device__ __forceinline__ void put(int which, float v) const
+    {
+        if ((threadIdx.x & 31) == 0) red[which][threadIdx.x >> 5] = v;
+        if (threadIdx.x < kMaxWarps && threadIdx.x >= nt / 32) red[which][threadIdx.x] = 0.0f;
+        __syncthreads();
+    }
 
     __device__ __forceinline__ float sum(int which, float v) const
     {
         v = warp_sum(v);
         if (nt == 32) return v;
-        if ((threadIdx.x & 31) == 0) red[which][threadIdx.x >> 5] = v;
-        __syncthreads();
+        put(which, v);
         const float4 *q = reinterpret_cast<const float4 *>(red[which]);
         const float4 a = q[0], b = q[1];
         float t = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));
@@ -181,10 +201,8 @@ struct Reds {
     {
         v = __reduce_max_sync(0xffffffffu, v);
         if (nt == 32) return v;
-        const int lane = threadIdx.x & 31;
-        if (lane == 0) red[which][threadIdx.x >> 5] = __uint_as_float(v);
-        __syncthreads();
-        return __reduce_max_sync(0xffffffffu, __float_as_uint(red[which][lane & (kMaxWarps - 1)]));
+        put(which, __uint_as_float(v));
+        return __reduce_max_sync(0xffffffffu, __float_as_uint(red[which][threadIdx.x & (kMaxWarps - 1)]));
     }
 
     // 1 / sqrt(mean(v^2) + eps).  Where squares leave the f32 range (above, or
@@ -229,6 +247,22 @@ __device__ __forceinline__ TokenGates load_gates(const Args &a, int t)
     return {a.y2_gate ? a.y2_gate[t] : 0.0f, a.gate_kind == HFQ_GATE_TOKEN ? a.gate[t] : 0.0f};
 }
 
+template <int NV>
+__device__ __forceinline__ void multiply_gate(const uint32_t (&g)[NV][8], bool sig, float (&b)[NV][8])
+{
+    if (sig) {
+#pragma unroll
+        for (int c = 0; c < NV; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b[c][i] *= sigmoid(__uint_as_float(g[c][i]));
+    } else {
+#pragma unroll
+        for (int c = 0; c < NV; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b[c][i] *= __uint_as_float(g[c][i]);
+    }
+}
+
 // One row, from its raw elements to its outputs.  The weights are the same for
 // every row: they are read where they are used, mostly from L1, and held no
 // longer, because registers decide how many rows an SM works on at once.
@@ -250,44 +284,34 @@ __device__ __forceinline__ void do_row(const Args &a, const Row<VEC, NV> &row, c
                 b[c][i] = R::template value<YB>(ry[c], i);
                 if (a.y2) b[c][i] = fmaf(g2, R::template value<YB>(ry2[c], i), b[c][i]);
             }
+        // what is one number for the row is multiplied once
+        float scale = a.beta;
+        if (a.gate_kind == HFQ_GATE_TOKEN) scale *= a.gate_sigmoid ? sigmoid(tg.gate) : tg.gate;
         if (a.w_post) {
-            const float r = red.template inv_rms<NV>(0, b, a.inv_h, a.eps);
-            uint32_t w[NV][8];
-            row.load_as(a.w_post, 0, a.w_bf16, w);
+            scale *= red.template inv_rms<NV>(0, b, a.inv_h, a.eps);
+            float w[NV][8];
+            row.load_weights(a.w_post, a.w_bf16, w);
 #pragma unroll
             for (int c = 0; c < NV; ++c)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    b[c][i] = b[c][i] * r *
-                              ((a.w_bf16 ? R::template value<true>(w[c], i) : R::template value<false>(w[c], i)) +
-                               a.w_offset);
+                for (int i = 0; i < 8; ++i) b[c][i] *= scale * (w[c][i] + a.w_offset);
+        } else {
+#pragma unroll
+            for (int c = 0; c < NV; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) b[c][i] *= scale;
         }
-        if (a.gate_kind == HFQ_GATE_TOKEN) {
-            const float g = a.gate_sigmoid ? sigmoid(tg.gate) : tg.gate;
-#pragma unroll
-            for (int c = 0; c < NV; ++c)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) b[c][i] *= g;
-        } else if (a.gate_kind != HFQ_GATE_NONE) {
-            const bool full = a.gate_kind == HFQ_GATE_FULL;
+        if (a.gate_kind == HFQ_GATE_FULL) multiply_gate<NV>(rg, a.gate_sigmoid, b);
+        else if (a.gate_kind == HFQ_GATE_CHANNEL) {
             uint32_t w[NV][8];
-            if (!full) row.template load<false>(a.gate, 0, w);
-#pragma unroll
-            for (int c = 0; c < NV; ++c)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float g = __uint_as_float(full ? rg[c][i] : w[c][i]);
-                    b[c][i] *= a.gate_sigmoid ? sigmoid(g) : g;
-                }
+            row.template load<false>(a.gate, 0, w);
+            multiply_gate<NV>(w, a.gate_sigmoid, b);
         }
+        // elements behind the row are 0 here, or NaN in a row that has none else
 #pragma unroll
         for (int c = 0; c < NV; ++c)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                x[c][i] = fmaf(a.beta, b[c][i], a.alpha * R::template value<XB>(rx[c], i));
-                // elements behind the row stay 0, whatever the gate's value made of them
-                if (!row.in(c, VEC ? 0 : i)) x[c][i] = 0.0f;
-            }
+            for (int i = 0; i < 8; ++i) x[c][i] = fmaf(a.alpha, R::template value<XB>(rx[c], i), b[c][i]);
         row.template store<XB>(a.x_out, (size_t)t * a.ldx, XB, x);
     } else {
 #pragma unroll
@@ -298,16 +322,19 @@ __device__ __forceinline__ void do_row(const Args &a, const Row<VEC, NV> &row, c
     }
     if (!a.xn && !a.xq) return;
     const float r = red.template inv_rms<NV>(2, x, a.inv_h, a.eps);
-    uint32_t w[NV][8];
-    if (a.w_pre) row.load_as(a.w_pre, 0, a.w_bf16, w);
+    if (a.w_pre) {
+        float w[NV][8];
+        row.load_weights(a.w_pre, a.w_bf16, w);
 #pragma unroll
-    for (int c = 0; c < NV; ++c)
+        for (int c = 0; c < NV; ++c)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            x[c][i] *= r;
-            if (a.w_pre)
-                x[c][i] *= (a.w_bf16 ? R::template value<true>(w[c], i) : R::template value<false>(w[c], i)) + a.w_offset;
-        }
+            for (int i = 0; i < 8; ++i) x[c][i] *= r * (w[c][i] + a.w_offset);
+    } else {
+#pragma unroll
+        for (int c = 0; c < NV; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[c][i] *= r;
+    }
     if (!a.xq) {
         row.template store<false>(a.xn, (size_t)t * a.H, a.xn_bf16, x);
         return;
@@ -362,10 +389,6 @@ __global__ void __launch_bounds__(NV * 256, NV > 1 ? 2 : VEC ? 5 : 3) norm_kerne
     if (a.y2) row.template load<YB>(a.y2, (size_t)t * a.ldy, y2);
     if (a.gate_kind == HFQ_GATE_FULL) row.template load<false>(a.gate, (size_t)t * a.H, g);
     const TokenGates tg = load_gates(a, t);
-    if (nt > 32) {
-        for (int i = threadIdx.x; i < kReds * kMaxWarps; i += nt) red[0][i] = 0.0f;
-        __syncthreads();
-    }
     do_row<VEC, NV, XB, YB>(a, row, Reds{red, nt}, t, x, y, y2, g, tg);
 }
 

@@ -51,6 +51,9 @@ __device__ __forceinline__ uint32_t cluster_rank()
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 
+// The same without a release: barriers set up with fence_mbar_init need none.
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void cluster_sync()
@@ -262,7 +265,7 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (a.split > 1) cluster_arrive();    // waited for before this CTA touches another's shared memory
+    if (a.split > 1) cluster_arrive_relaxed();       // waited for before this CTA touches another's shared memory
     dependency_wait();
     let_next_begin();
     const uint32_t tmem = tmem_base;
@@ -538,7 +541,8 @@ q8_pair_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
     }
     tc_fence_before_sync();
     __syncthreads();
-    cluster_sync();
+    cluster_arrive_relaxed();
+    cluster_wait();
     tc_fence_after_sync();
     const uint32_t tmem = tmem_base;
     volatile int *abortp = &abort_flag;
@@ -623,7 +627,8 @@ q8_pair_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
-    cluster_sync();                                      // the other CTA may still arrive on barriers here
+    cluster_arrive_relaxed();                            // the other CTA may still arrive on barriers here
+    cluster_wait();
     tc_fence_after_sync();
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kCols) : "memory");
