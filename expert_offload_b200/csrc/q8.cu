@@ -303,16 +303,17 @@ cudaError_t launch_dot(const DotArgs &a, int smem, cudaStream_t s)
     return launch_ordered(dot_kernel<TT, R>, (a.m.N + per - 1) / per, kDotWarps * 32, smem, s, a);
 }
 
-// One or two tokens and few weights: the dot kernel's short start wins (2.9 us
-// against 4 us and more for one token of 2048 x 1024); with more of either the
-// tensor cores' stream of weights does (17 us against 30 at 8192 x 8192).
+// One or two tokens and few weights: the dot kernel's short start wins (2.8
+// and 3.8 us for one and two tokens of 2048 x 1024, where the fused kernel takes
+// 4.8); with more of either the tensor cores' stream of weights does (17 us
+// against 28 at 8192 x 8192).
 bool takes_dot(int T, int K, int N) { return T <= 2 && (long long)K * N * T <= (4 << 20); }
 
-// Up to eight tokens and few weights: the fused kernel, one launch for two.  With
-// more weights the quantiser's own kernel, beside which the product starts its
-// weights, is 1 to 2 us quicker on the GPU (18.4 against 20.8 us for 5 tokens of
-// 8192 x 8192, 8.0 against 9.1 of 2048 x 8192) and pays for its launch.
-bool takes_fused(int T, int K, int N) { return T <= kQ8FusedTokens && (long long)K * N <= (8 << 20); }
+// Up to eight tokens and few weights: the fused kernel, one launch (and 2 us of
+// host time) less.  With more weights the quantiser's own kernel, beside which
+// the product starts its weights, is quicker on the GPU (16.9 against 19.0 us for
+// 5 tokens of 8192 x 8192; 7.1 against 7.2 of 2048 x 8192).
+bool takes_fused(int T, int K, int N) { return T <= kQ8FusedTokens && (long long)K * N <= (16 << 20); }
 
 hfq_status run_dot(const DotArgs &a, cudaStream_t s)
 {

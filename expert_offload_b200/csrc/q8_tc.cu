@@ -195,9 +195,8 @@ __device__ __forceinline__ void store_columns(const Q8Mat &m, int t0, int n, int
 // (every CTA of its share of K, the shares' maxima exchanged through the
 // cluster), and write the CTA's share of the quantised rows where the MMAs read
 // them, in the 128-byte swizzle that a TMA load would have given them.  One
-// launch, and x is read from L2 by every channel tile, which is cheaper than
-// a kernel before this one: 16 tokens of a 2048 x 1024 product took 5.7 us with
-// the quantiser before them.
+// launch; x is read from L2 by every channel tile.  5 tokens of 2048 x 1024 take
+// 5.0 us, of 2048 x 8192 (17 MB of weights, 2.6 us) 7.2.
 constexpr int kFew = 16;                  // tokens of its tile
 constexpr int kShare = 24;                // its stages of K: 48 KB of quantised tokens
 constexpr int kQuantWarps = 8;
@@ -709,9 +708,11 @@ cudaError_t launch_pair(const Args &a, const CUtensorMap &wmap, const CUtensorMa
 // CTAs of a cluster for tiles of bt tokens.  Splitting K shortens each CTA's
 // run through it (0.27 us a stage) and puts more of the memory system to work,
 // up to two CTAs on an SM; it costs the exchange of the sums (about 1.5 us for
-// 64 tokens), so a tile of many tokens is split only if K is long: with tiles
-// on half of the SMs, 16 stages lose (12.1 us for 11.4 at 128 x 2048 x 8192),
-// 64 gain (23.8 for 28.7 at 512 x 8192 x 2048).
+// 64 tokens), so a tile of many tokens is split only if K is long.  Tokens x K x
+// N, one tile of K a CTA against the split: with tiles on most SMs 16 stages
+// lose (128 x 2048 x 8192: 11.4 us and 12.1), 64 gain (512 x 8192 x 2048: 28.7
+// and 23.8); with few tiles 4 stages lose (256 x 512 x 2048: 6.8 and 8.6), 16
+// gain (256 x 2048 x 1024: 11.2 and 9.0).
 static int split_of(int bt, int tiles, int nk)
 {
     const int sms = sm_count(), least = bt == kFew ? 1 : 2;

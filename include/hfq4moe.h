@@ -45,8 +45,13 @@
  *     hfq_last_error() returns a thread-local message for the last failure.
  *     Device-side conditions (a bounded wait that ran out) are written to a
  *     status word in the workspace and read by hfq_workspace_status().
+ *   - Order: calls on one stream take effect in their order, as kernels do.
+ *     moe_route_scored, moe_norm_residual and the 8-bit products are set up
+ *     while their predecessor on the stream still runs (programmatic
+ *     dependent launch) and wait for it before they touch memory.
  *   - Limits: 1 <= k <= 16, k <= E <= 512, H and I multiples of 128
- *     (H, I <= 8192), T <= 65536, pointers 16-byte aligned.
+ *     (H, I <= 8192), T <= 65536, pointers 16-byte aligned, unless an entry
+ *     point names its own.
  */
 #ifndef HFQ4MOE_H
 #define HFQ4MOE_H
@@ -192,11 +197,11 @@ hfq_status moe_router_logits(const void *x, hfq_dtype x_dtype, int T, int hidden
  *   logits:  [T][n_experts] in logits_dtype, rows ld elements apart (0 =
  *            n_experts; else ld >= n_experts), aligned to their type.
  *   bias:    f32 [n_experts] or NULL.
- *   idx, wts, cnt, off, perm, workspace: as for moe_route;
- *            moe_route_scored_workspace_bytes(T, E, k) bytes, 16-byte
- *            aligned, needed only with the lists (it may be NULL when that
- *            is 0), with no state kept between calls.  Calls that share a
- *            workspace must be ordered.
+ *   idx, wts, cnt, off, perm: as for moe_route.
+ *   workspace: needed only with the lists, moe_route_scored_workspace_bytes(T,
+ *            E, k) bytes, 16-byte aligned (it may be NULL when that is 0: up
+ *            to 16 tokens), with any contents; nothing in it is kept between
+ *            calls, and calls that share it must be ordered.
  *   Limits: n_groups <= 32 and divides n_experts; 1 <= topk_groups <=
  *            n_groups; group_top 1 or 2 and <= n_experts / n_groups;
  *            k <= topk_groups * n_experts / n_groups; scale finite.
@@ -229,11 +234,12 @@ hfq_status moe_route_scored(const void *logits, hfq_dtype logits_dtype, int ld, 
  *     xn  = x' * rsqrt(mean(x'^2) + eps) * (w_pre + w_offset)  -> xn, and in
  *           8 bits -> xq, xq_scale
  *   y NULL: no block behind the row: x' = x, nothing of the first three lines
- *   is done (y2 and gate must be NULL), the plain norm before the first block.
+ *   is done (y2 and gate must be NULL, the rule's gate_kind and w_post do not
+ *   count), the plain norm before the first block.
  *   x' is rounded to x's type before it is normed, so that xn is the norm of
- *   what x_out holds.  All arithmetic is f32 (a row whose sum of squares
- *   leaves the f32 range is summed again at another scale); one rounding per
- *   output.  NaN and infinities of a row stay in that row.
+ *   what x_out holds.  All arithmetic is f32 (a row whose squares leave the
+ *   f32 range is summed again at another scale); one rounding per output.  NaN
+ *   and infinities of a row stay in that row.
  *   x:       [T][H] in x_dtype, rows ldx elements apart (0 = H).
  *   y, y2:   [T][H] in y_dtype, rows ldy elements apart (0 = H).
  *   y2_gate: f32 [T], logits of the second branch's gate, or NULL.
@@ -241,7 +247,7 @@ hfq_status moe_route_scored(const void *logits, hfq_dtype logits_dtype, int ld, 
  *            [T][H] (HFQ_GATE_FULL); NULL with HFQ_GATE_NONE.  gate_act:
  *            HFQ_GATE_LINEAR (as it is) or HFQ_GATE_SIGMOID.
  *   x_out:   [T][H] in x_dtype, rows ldx apart, or NULL; it may be x itself
- *            (x_out == x), else it must not overlap an input.
+ *            (x_out == x).  Else no output may overlap an input or another.
  *   xn:      contiguous [T][H] in xn_dtype, or NULL.  w_pre NULL with xn or
  *            xq: the bare norm (a weight of 1).
  *   xq, xq_scale: int8 [T][round16(H)] (round16: up to a multiple of 16; the
@@ -251,8 +257,8 @@ hfq_status moe_route_scored(const void *logits, hfq_dtype logits_dtype, int ld, 
  *   w_post, w_pre: [H] in w_dtype.
  *   At least one of x_out, xn and xq is wanted.  1 <= H <= 8192,
  *   1 <= T <= 65536, eps >= 0, every scale finite, pointers aligned to their
- *   type.  Rows whose addresses are all 16-byte aligned, with H a multiple of
- *   8, are read 16 bytes at a time.
+ *   type (xq to 16 bytes).  Quickest: H a multiple of 8, and rows that start on
+ *   16 bytes (bf16) or 32 (f32).
  */
 #define HFQ_GATE_NONE 0
 #define HFQ_GATE_TOKEN 1
@@ -299,15 +305,20 @@ hfq_status moe_norm_residual(const moe_norm_rule *rule, int T, int H, const void
  * q8_matmul: y[t][n] = (sum_k xq[t][k] * wq[n][k]) * xs[t] * ws[n], the sum
  * exact in 32-bit integers, the rest f32 with one rounding to y's type.
  *   xq, wq: int8 [T][K], [N][K], rows ldxq, ldw bytes apart (0 = round16(K);
- *           else a multiple of 16, >= K), 16-byte aligned; bytes behind K are
- *           not used.  Any value of -128 .. 127 may stand in them.
+ *           else a multiple of 16, >= K), 16-byte aligned, every row, the last
+ *           too, of round16(K) readable bytes; what those behind K hold does
+ *           not count.  Any value of -128 .. 127 may stand in them.
  *   y:      [T][N] in y_dtype, rows ldy elements apart (0 = N; else >= N).
  *
  * q8_linear: y = q8_matmul(q8_quantize_rows(x), wq): the same bits as the two
  * calls, in one launch where the tokens are few.
  *   workspace: q8_linear_workspace_bytes(T, K, N) bytes of device scratch
- *           (may be NULL when that is 0), 256-byte aligned, with no state kept
- *           between calls; calls that share one must be ordered.
+ *           (may be NULL when that is 0), 256-byte aligned, with any contents;
+ *           nothing in it is kept between calls, and calls that share it must
+ *           be ordered.
+ *   The tensor-core kernels' waits are bounded (HFQ_OPT_WAIT_TIMEOUT_NS); one
+ *   that ran out is reported by hfq_workspace_status(NULL, 0, stream), and the
+ *   product's output is undefined.
  *   Limits: 1 <= T, rows <= 65536, 1 <= K, cols <= 16384, 1 <= N <= 65536;
  *           x and y aligned to their type.
  */
@@ -460,7 +471,9 @@ hfq_status hfq4_moe_forward_noalloc(const hfq4_layer *layer, const void *x, hfq_
  *     persistent-kernel launch makes its grid barriers wait for this many
  *     CTAs that do not exist (the one-token kernel, which has no grid
  *     barrier: makes its layer-1 input poll, or with one layer its h poll,
- *     expect a tag nobody writes), so the wait runs out without any fault.
+ *     expect a tag nobody writes; a tensor-core 8-bit product: makes its MMA
+ *     warp wait for an arrival that never comes), so the wait runs out without
+ *     any fault.
  *   HFQ_OPT_TIMELINE_BUFFER: debug; the device address of a u64 buffer of
  *     n_sms * n_layers * 32 words, zero-filled (0 = off).  Persistent-kernel
  *     launches then write %globaltimer stamps (ns), per layer l at word
@@ -488,8 +501,9 @@ hfq_status hfq_set_option(int option, long long value);
  * work of such a pair is skipped, its output left unwritten.  After an error
  * the word and the workspace's control block are cleared.  A new workspace
  * must be zero-filled before its first use.  workspace = NULL with
- * ws_bytes = 0 reads the status word of hfq4_moe_forward_noalloc's array on
- * the current device (HFQ_OK when no such call has run there).
+ * ws_bytes = 0 reads the status words of what has no workspace on the current
+ * device: the 8-bit products, then hfq4_moe_forward_noalloc's array (HFQ_OK
+ * when no such call has run there).
  */
 hfq_status hfq_workspace_status(void *workspace, size_t ws_bytes, void *stream);
 
