@@ -22,6 +22,14 @@ constexpr int kKb = 128;                  // K of a stage: one swizzled row of 1
 constexpr int kMaxStages = 12;            // of a tile kernel's ring
 constexpr int kSmemFull = 222 * 1024;     // dynamic shared memory of a CTA that has an SM to itself
 constexpr int kSmemHalf = 110 * 1024;     // of one of two
+// CTAs of a cluster wait for one another while they hold tensor memory.  So that
+// two kernels on different streams cannot each hold what the other's CTAs wait
+// for, a CTA pair (all 512 columns) leaves no shared memory for another CTA on
+// its SM, and a CTA of a cluster takes enough of it that it cannot sit beside one
+// of a kernel that fills an SM; what then fits beside each other stays below 512
+// columns.
+constexpr int kSmemPair = 224 * 1024;
+constexpr int kSmemCluster = 72 * 1024;
 
 __device__ unsigned g_status;             // HFQ_ERR_TIMEOUT after a wait ran out
 
@@ -453,7 +461,8 @@ struct PairCfg {
     static constexpr int kBT = 256;                                  // tokens of a tile
     static constexpr int kA = kCh * kKb, kB = kBT / 2 * kKb, kStage = kA + kB;
     static constexpr int kStages = 6;
-    static constexpr int kSmem = 1024 + kStages * kStage;
+    static constexpr int kSmem = kSmemPair;
+    static_assert(1024 + kStages * kStage <= kSmem, "the ring fits");
     static constexpr uint32_t kCols = 2 * kBT;
 };
 
@@ -679,7 +688,7 @@ cudaError_t launch_tile(Args a, const CUtensorMap &wmap, const CUtensorMap &xmap
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((a.m.N + kCh - 1) / kCh * a.split, (a.m.T + BT - 1) / BT);
     cfg.blockDim = dim3(C::kThr);
-    cfg.dynamicSmemBytes = fixed + a.stages * C::kStage;
+    cfg.dynamicSmemBytes = std::max(fixed + a.stages * C::kStage, a.split > 1 ? kSmemCluster : 0);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -19,7 +19,8 @@
 // decided in 64 bits from the start (select64).
 // Without a bias the logits decide, which are exact as they are.
 //
-// Bound by instructions: one token of 512 experts is about 600 of a warp.
+// Bound by instructions: a token of 512 experts in 8 groups is 1170 of a warp,
+// with its pairs counted (8192 tokens: 14.4 us without lists, 26.4 with them).
 #include <algorithm>
 #include <cfloat>
 

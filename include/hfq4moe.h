@@ -319,6 +319,7 @@ hfq_status moe_norm_residual(const moe_norm_rule *rule, int T, int H, const void
  *   The tensor-core kernels' waits are bounded (HFQ_OPT_WAIT_TIMEOUT_NS); one
  *   that ran out is reported by hfq_workspace_status(NULL, 0, stream), and the
  *   product's output is undefined.
+ *   No output may overlap an input or another output.
  *   Limits: 1 <= T, rows <= 65536, 1 <= K, cols <= 16384, 1 <= N <= 65536;
  *           x and y aligned to their type.
  */

@@ -265,6 +265,47 @@ def test_captured_another_stream_and_twice_the_same_bits(eo, T):
     assert torch.equal(ys[0], ys[2]) and not torch.equal(ys[0], ys[1])
 
 
+def test_products_on_two_streams_at_once(eo):
+    """CTA pairs, which take all of an SM's tensor memory, beside clusters that
+    split K, and the other kernels beside both: each stream's results are those
+    that it has alone."""
+    shapes = [[(1024, 512, 4096), (1024, 2048, 4096)], [(16, 2048, 1024), (40, 1024, 2048), (5, 2048, 1024)],
+              [(300, 128, 3000), (2, 1024, 1024)]]
+    streams = [torch.cuda.Stream() for _ in shapes]
+    calls, alone = [], []
+    for i, group in enumerate(shapes):
+        mine = []
+        for T, K, N in group:
+            x = _randn(T + i, T, K, dt="bf16")
+            w, ws = _weights(N + i, N, K, K)
+            work = torch.zeros(eo.q8_linear_workspace_bytes(T, K, N) or 1, dtype=torch.uint8, device="cuda")
+            mine.append((x, T, K, w, ws, N, torch.zeros(T, N, device="cuda"), work))
+        calls.append(mine)
+
+    def run(c, stream):
+        x, T, K, w, ws, N, y, work = c
+        eo.q8_linear(x, eo.HFQ_BF16, T, K, w, ws, N, y, eo.HFQ_F32, work, stream=stream)
+
+    for mine in calls:
+        for c in mine:
+            run(c, None)
+    torch.cuda.synchronize()
+    alone = [[c[6].clone() for c in mine] for mine in calls]
+    for mine in calls:
+        for c in mine:
+            c[6].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for mine, s in zip(calls, streams):
+            for c in mine:
+                run(c, s)
+    torch.cuda.synchronize()
+    eo.hfq_workspace_status(None)
+    for mine, want in zip(calls, alone):
+        for c, y in zip(mine, want):
+            assert torch.equal(c[6], y)
+
+
 def test_offsets_past_32_bits(eo):
     """An output of more than 2^32 bytes: its last rows and channels."""
     T, K, N = 40000, 32, 65536
