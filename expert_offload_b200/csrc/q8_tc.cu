@@ -28,7 +28,7 @@ constexpr int kSmemHalf = 110 * 1024;     // of one of two
 // its SM, and a CTA of a cluster takes enough of it that it cannot sit beside one
 // of a kernel that fills an SM; what then fits beside each other stays below 512
 // columns.
-constexpr int kSmemPair = 224 * 1024;
+constexpr int kSmemPair = 222 * 1024;
 constexpr int kSmemCluster = 72 * 1024;
 
 __device__ unsigned g_status;             // HFQ_ERR_TIMEOUT after a wait ran out
@@ -121,8 +121,9 @@ __device__ bool wait_bar(uint64_t *bar, uint32_t parity, long long timeout_ns, v
     }
 }
 
-// 32 consecutive columns of this thread's tensor-memory lane.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, int (&v)[32])
+// 32 consecutive columns of this thread's tensor-memory lane; they are there
+// after tmem_ld_wait().
+__device__ __forceinline__ void tmem_ld32_begin(uint32_t taddr, int (&v)[32])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
                  "%13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, "
@@ -133,6 +134,11 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, int (&v)[32])
                    "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]),
                    "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
                  : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, int (&v)[32])
+{
+    tmem_ld32_begin(taddr, v);
     tmem_ld_wait();
 }
 
@@ -519,7 +525,7 @@ q8_pair_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
     extern __shared__ uint8_t raw[];
     uint8_t *buf = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], never;
-    __shared__ __align__(16) float xs_of[kEpiWarps][32];
+    __shared__ __align__(16) float xs_of[kEpiWarps][C::kBT / kEpiParts];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -611,24 +617,33 @@ q8_pair_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
             int c, t;
             tile_of(i, ct, tt, c, t);
             const int b = n & 1, nn = c * 2 * kCh + rank * kCh + ch, t0 = t * BT;
+            // the scales of the part's tokens, while the MMAs still run
             const float ws = nn < m.N ? __ldg(m.ws + nn) : 0.0f;
+            float *xs = xs_of[warp - 2];
+            __syncwarp();                                    // the last tile's have been read
+#pragma unroll
+            for (int j = 0; j < kPart; j += 32) {
+                const int at = t0 + part * kPart + j + lane;
+                xs[j + lane] = at < m.T ? __ldg(m.xs + at) : 0.0f;
+            }
+            __syncwarp();
             if (!wait_bar(&tfull[b], (uint32_t)(n / 2) & 1u, a.timeout_ns, abortp)) break;
             tc_fence_after_sync();
-#pragma unroll 1
-            for (int col = part * kPart; col < (part + 1) * kPart; col += 32) {
-                int v[32];
-                tmem_ld32(trow + (uint32_t)(b * BT + col), v);
-                if (col + 32 == (part + 1) * kPart) {     // this warp's last read of the buffer
+            // 32 columns at a time, the next ones on their way out of tensor memory
+            const uint32_t src = trow + (uint32_t)(b * BT + part * kPart);
+            int v[2][32];
+            tmem_ld32_begin(src, v[0]);
+#pragma unroll
+            for (int j = 0; j < kPart / 32; ++j) {
+                tmem_ld_wait();
+                if (j + 1 < kPart / 32) tmem_ld32_begin(src + 32 * (j + 1), v[(j + 1) & 1]);
+                else {                                       // this warp's last read of the buffer is done
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(map_rank(smem_u32(&tempty[b]), 0));
                 }
-                const int tc = t0 + col;
-                if (tc >= m.T) continue;
-                __syncwarp();                                // the last columns' scales have been read
-                xs_of[warp - 2][lane] = tc + lane < m.T ? __ldg(m.xs + tc + lane) : 0.0f;
-                __syncwarp();
-                store_columns(m, tc, nn, lane, pairs, ws, xs_of[warp - 2], v);
+                const int tc = t0 + part * kPart + 32 * j;
+                if (tc < m.T) store_columns(m, tc, nn, lane, pairs, ws, xs + 32 * j, v[j & 1]);
             }
         }
     }
