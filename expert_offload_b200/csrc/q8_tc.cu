@@ -223,7 +223,7 @@ struct TileCfg {
     static constexpr int kA = kCh * kKb, kB = BT * kKb, kStage = FUSED ? kA : kA + kB;
     static constexpr int kExch = kCh * BT * 4;                       // bytes of the exchange
     static constexpr int kThr = FUSED ? 64 + 32 * kQuantWarps : 192; // TMA warp, MMA warp, the others
-    static constexpr uint32_t kCols = BT < 32 ? 32 : BT;             // tensor-memory columns
+    static constexpr int kCols = BT < 32 ? 32 : BT;                  // tensor-memory columns
 };
 
 template <int BT, int MODE>
@@ -237,7 +237,7 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
     uint8_t *xbuf = buf + a.stages * C::kStage;                      // FUSED: [share][kB]
     uint8_t *ebuf = xbuf + (FUSED ? a.share * C::kB : 0);            // the exchange
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done, never, xready, amax_bar;
-    __shared__ __align__(16) float xs_of[4][32];
+    __shared__ __align__(16) float xs_of[4][C::kCols];
     __shared__ uint32_t top_in[8][kFew], top[kFew];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -381,27 +381,33 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
         }
         if (warp < 6) {
             // the sums: warp w reads lanes 32 (w % 4) .. + 31
-            const bool ok = wait_bar(&done, 0u, a.timeout_ns, abortp);
-            __syncwarp();
-            tc_fence_after_sync();
             const int ch = (warp & 3) * 32 + lane, n = n0 + ch;
             const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
             const int tv = min(BT, m.T - t0);
+            // the scales, while the MMAs still run
+            float *xs = xs_of[warp - 2];
+            const float ws = a.split == 1 && n < m.N ? __ldg(m.ws + n) : 0.0f;
+            if (!FUSED && a.split == 1)
+#pragma unroll
+                for (int j = 0; j < BT; j += 32) xs[j + lane] = j + lane < tv ? __ldg(m.xs + t0 + j + lane) : 0.0f;
+            const bool ok = wait_bar(&done, 0u, a.timeout_ns, abortp);
+            __syncwarp();
+            tc_fence_after_sync();
             if (__all_sync(0xffffffffu, ok)) {
                 if (a.split == 1) {
                     const bool pairs = m.y_bf16 && m.ldy % 2 == 0 && ((uintptr_t)m.y & 3) == 0;
-                    const float ws = n < m.N ? m.ws[n] : 0.0f;
-#pragma unroll 1
-                    for (int col = 0; col < tv; col += 32) {
-                        int v[32];
-                        tmem_ld32(trow + col, v);
-                        __syncwarp();                        // the last columns' scales have been read
-                        xs_of[warp - 2][lane] = col + lane >= tv ? 0.0f
-                                                : FUSED          ? row_scale(top[lane])
-                                                                 : __ldg(m.xs + t0 + col + lane);
-                        __syncwarp();
-                        store_columns(m, t0 + col, n, lane, pairs, ws, xs_of[warp - 2], v);
+                    if (FUSED) xs[lane] = lane < tv ? row_scale(top[lane]) : 0.0f;
+                    __syncwarp();
+                    int v[2][32];
+                    tmem_ld32_begin(trow, v[0]);
+#pragma unroll
+                    for (int col = 0; col < C::kCols; col += 32) {
+                        if (col >= tv) break;
+                        tmem_ld_wait();
+                        if (col + 32 < C::kCols) tmem_ld32_begin(trow + col + 32, v[(col / 32 + 1) & 1]);
+                        store_columns(m, t0 + col, n, lane, pairs, ws, xs + col, v[(col / 32) & 1]);
                     }
+                    tmem_ld_wait();
                 } else {
                     // four tokens of a channel are 16 bytes, next to those of the next
                     // channel: a warp's store is one run of 512 bytes for each owner
