@@ -238,7 +238,8 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
     uint8_t *ebuf = xbuf + (FUSED ? a.share * C::kB : 0);            // the exchange
     __shared__ uint64_t full[kMaxStages], empty[kMaxStages], done, never, xready, amax_bar;
     __shared__ __align__(16) float xs_of[4][C::kCols];
-    __shared__ uint32_t top_in[8][kFew], top[kFew];
+    __shared__ uint32_t top_in[8][kFew];
+    __shared__ float ws_own[kCh], xs_own[BT];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, stages = a.stages;
@@ -364,7 +365,7 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
                     wait_bar(&amax_bar, 0u, a.timeout_ns, abortp);
                     big = __reduce_max_sync(0xffffffffu, lane < a.split ? top_in[lane][t] : 0u);
                 }
-                if (lane == 0) top[t] = big;
+                if (lane == 0) xs_own[t] = row_scale(big);
                 const RowQuant<BF16> q(big);
 #pragma unroll 1
                 for (int k = k0 + 8 * lane; k < k1; k += 256) {
@@ -396,7 +397,7 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
             if (__all_sync(0xffffffffu, ok)) {
                 if (a.split == 1) {
                     const bool pairs = m.y_bf16 && m.ldy % 2 == 0 && ((uintptr_t)m.y & 3) == 0;
-                    if (FUSED) xs[lane] = lane < tv ? row_scale(top[lane]) : 0.0f;
+                    if (FUSED) xs[lane] = lane < tv ? xs_own[lane] : 0.0f;
                     __syncwarp();
                     int v[2][32];
                     tmem_ld32_begin(trow, v[0]);
@@ -428,9 +429,14 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
         }
     }
     if (a.split > 1) {
+        // the scales of this CTA's outputs, beside the others' last sums
+        const int own = kCh / a.split, tv = min(BT, m.T - t0);
+        for (int i = threadIdx.x; i < own + (FUSED ? 0 : tv); i += C::kThr) {
+            if (i < own) ws_own[i] = n0 + rank * own + i < m.N ? __ldg(m.ws + n0 + rank * own + i) : 0.0f;
+            else xs_own[i - own] = __ldg(m.xs + t0 + i - own);
+        }
         __syncwarp();
         cluster_sync();
-        const int own = kCh / a.split, tv = min(BT, m.T - t0);
         const int4 *part = reinterpret_cast<const int4 *>(ebuf);
         for (int i = threadIdx.x; i < own * ((tv + 3) / 4); i += C::kThr) {
             const int q = i / own, c = i - q * own, n = n0 + rank * own + c;
@@ -440,13 +446,10 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
                 const int4 p = part[r * own * (BT / 4) + i];
                 sum[0] += p.x, sum[1] += p.y, sum[2] += p.z, sum[3] += p.w;
             }
-            const float ws = __ldg(m.ws + n);
+            const float ws = ws_own[c];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (4 * q + j < tv) {
-                    const int t = t0 + 4 * q + j;
-                    store_y(m, t, n, q8_value(sum[j], FUSED ? row_scale(top[4 * q + j]) : __ldg(m.xs + t), ws));
-                }
+                if (4 * q + j < tv) store_y(m, t0 + 4 * q + j, n, q8_value(sum[j], xs_own[4 * q + j], ws));
         }
     }
     tc_fence_before_sync();
