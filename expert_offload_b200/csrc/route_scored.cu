@@ -348,7 +348,9 @@ __device__ __forceinline__ Slot select_token(const Args &a, size_t row, const fl
                 t1 = fmaxf(t1, o1);
             }
             const bool two = a.group_top > 1 && t2 > -INFINITY;
-            const float g = grp < a.n_groups ? (two ? t1 + t2 : t1) : -INFINITY;
+            // two of the lowest biases add up to -inf in 32 bits, which is for groups
+            // without a live expert
+            const float g = grp < a.n_groups ? (two ? fmaxf(t1 + t2, -FLT_MAX) : t1) : -INFINITY;
             int ahead = 0;
             for (int q = 0; q < a.n_groups; ++q) {
                 const float h = __shfl_sync(0xffffffffu, g, q * a.tpl);
@@ -363,7 +365,8 @@ __device__ __forceinline__ Slot select_token(const Args &a, size_t row, const fl
                 const float err = 2.0f * base + kU * redux_max(off);
                 // -inf on the outside: those groups have no live expert
                 if (out > -INFINITY && !(in - out > 2.0f * err)) {
-                    const float low = (a.group_top > 1 ? (two ? t2 : t1) : t1) - 2.0f * err;
+                    // -inf, too, where both are infinite
+                    const float low = fmaxf((two ? t2 : t1) - 2.0f * err, -INFINITY);
                     const int kept = groups64<N>(a, row, low, lane, m, zi, cand);
                     if (kept < 0) return select64<N>(a, row, lane, m);
                     keep = kept;
@@ -480,7 +483,6 @@ __device__ __forceinline__ void read_bias(const Args &a, int e0, int n, float (&
 }
 
 // The lane's logits as they are (-inf behind its run).
-
 template <int N>
 __device__ __forceinline__ void load_logits(const Args &a, size_t row, int e0, int n, float (&l)[N])
 {

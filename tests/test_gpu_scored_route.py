@@ -249,3 +249,28 @@ def test_lists_of_every_chunk_size(eo, T, E, k):
     np.testing.assert_array_equal(got[2], cnt)
     np.testing.assert_array_equal(got[3], np.concatenate([[0], np.cumsum(cnt)]))
     np.testing.assert_array_equal(got[4], np.argsort(flat, kind="stable"))
+
+
+@pytest.mark.parametrize("score", [0, 1], ids=["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,n", [(8, 2), (16, 4), (24, 3), (64, 8), (256, 8), (510, 17)])
+def test_biases_of_the_ends_of_the_range(eo, score, E, n):
+    """Biases of f32's lowest and largest values and of +inf: two of them add up
+    to an infinity in 32 bits, and infinities have no distance."""
+    size, big, inf = E // n, float(np.finfo(np.float32).max), float("inf")
+    l = _rand(9, E, E + n)
+    l[5, : E // 2] = -inf
+    rng = np.random.default_rng(E)
+    for gt in (1, 2):
+        for tg in {1, n // 2, n - 1}:
+            rule = dict(score=score, n_groups=n, topk_groups=tg, group_top=gt)
+            for values in ([-big], [-big, -inf], [big], [inf], [big, inf], [-big, 0.0], [inf, 0.0], [-big, big, -inf],
+                           [-big, inf, 0.25, -inf]):
+                each = torch.from_numpy(rng.choice(np.float32(values), E)).cuda()
+                lead = torch.full((E,), values[0], device="cuda")
+                lead[:size] = values[-1]                 # the first group unlike the others
+                last = lead.flip(0)
+                for bias in (each, lead, last):
+                    _check(eo, l, min(3, tg * size), rule, bias=bias)
+                    # every bias of a group one value, of the groups in turn
+                by_group = torch.tensor(values, device="cuda")[torch.arange(E, device="cuda") // size % len(values)]
+                _check(eo, l, min(3, tg * size), rule, bias=by_group)
