@@ -207,7 +207,8 @@ struct Reds {
 
     // 1 / sqrt(mean(v^2) + eps).  Where squares leave the f32 range (above, or
     // below with an eps that does not cover it) the row is scaled, in v, too, and
-    // summed again.
+    // summed again: a small one by 2^86, which takes the square of the least f32
+    // to 2^-126 and a sum below 2^-60 to less than 2^112.
     template <int NV>
     __device__ __forceinline__ float inv_rms(int which, float (&v)[NV][8], float inv_h, float eps) const
     {
@@ -219,7 +220,7 @@ struct Reds {
         s = sum(which, s);
         const bool small = s < 0x1p-60f && eps < 0x1p-60f;
         if (!(s <= FLT_MAX) || small) {
-            const float f = small ? 0x1p64f : 0x1p-80f;
+            const float f = small ? 0x1p86f : 0x1p-80f;
             s = 0.0f;
 #pragma unroll
             for (int c = 0; c < NV; ++c)

@@ -212,6 +212,22 @@ def test_rows_at_the_ends_of_the_f32_range(eo, H):
         c.call().check()
 
 
+@pytest.mark.parametrize("H", [1, 64, 1001, 8192])
+def test_rows_of_the_least_f32_values(eo, H):
+    """Below 2^-126, where a value has few bits left but its norm has them all."""
+    for scale in (2.0 ** -126, 2.0 ** -140, 2.0 ** -149):
+        c = Case(eo, 3, H, "f32", "f32", branch=False, eps=0.0)
+        c.x.copy_(torch.round(c.x / c.x.abs().max() * 2.0 ** 9).double() * scale)
+        c.x[::H] = 2.0 ** -149                           # no row of zeros
+        assert (c.x.view(3, H) != 0).any(1).all() and float(c.x.abs().max()) <= 2.0 ** 9 * scale
+        c.x0 = c.x.clone()
+        c.call().check()
+        c = Case(eo, 3, H, "f32", "f32", eps=0.0)        # the branch's own norm
+        c.y.copy_(torch.round(c.y / c.y.abs().max() * 2.0 ** 9).double() * scale)
+        c.y[::H] = 2.0 ** -149
+        c.call().check()
+
+
 def test_a_rule_with_a_gate_serves_a_row_without_a_block(eo):
     """A gate's kind says nothing where there is no block: the plain norm."""
     for gate in ("token", "channel", "full"):
