@@ -298,19 +298,22 @@ class NormRule:
         self.struct = moe_norm_rule(_ptr(w_post), _ptr(w_pre), w_dtype, eps, w_offset, residual_scale,
                                     branch_scale, gate_kind, gate_act)
         self.address = ctypes.addressof(self.struct)
-        self.checked = 0                 # elements that the weights are known to have
+        self.tensors = any(w is not None and type(w) is not int for w in (w_post, w_pre))
+        self.checked = 0                 # elements that the weights are known to have ...
+        self.device = None               # ... on this device
 
     def check(self, H: int) -> None:
         """The weights hold H elements of their type on the current device; they
-        are the rule's own, so once is enough for each length."""
+        are the rule's own, so once is enough for each length and device."""
         for name, w in (("w_post", self.w_post), ("w_pre", self.w_pre)):
             if w is None or type(w) is int:
                 continue
             torch = sys.modules.get("torch")
             kinds = (torch.float32,) if self.w_dtype == HFQ_F32 else (torch.bfloat16, torch.int16, torch.uint16)
-            if not w.is_cuda or w.dtype not in kinds:
-                raise HfqError(-1, f"{name} is not a CUDA tensor of the rule's w_dtype")
+            if not w.is_cuda or w.get_device() != torch._C._cuda_getDevice() or w.dtype not in kinds:
+                raise HfqError(-1, f"{name} is not a tensor of the current CUDA device of the rule's w_dtype")
             _strided(name, w, H)
+            self.device = w.get_device()
         self.checked = H
 
 
@@ -318,7 +321,7 @@ def moe_norm_residual(rule: NormRule, T: int, H: int, x, x_dtype: int, y=None, y
                       y2=None, y2_gate=None, gate=None, x_out=None, xn=None, xn_dtype: int = HFQ_BF16,
                       xq=None, xq_scale=None, ldx: int = 0, ldy: int = 0, stream=None) -> None:
     """x' = residual_scale x + branch_scale gate norm(y + y2), xn = norm(x')."""
-    if rule.checked < H:
+    if rule.tensors and (rule.checked < H or rule.device != sys.modules["torch"]._C._cuda_getDevice()):
         rule.check(H)
     nx, ny = (T - 1) * (ldx or H) + H, (T - 1) * (ldy or H) + H
     kind = rule.gate_kind

@@ -177,7 +177,10 @@ static PyObject *call(PyObject *self, PyObject *const *args, Py_ssize_t n)
             }
         }
     }
-    const hfq_status st = g_calls[which].fn(v);
+    hfq_status st;
+    Py_BEGIN_ALLOW_THREADS                       /* a launch waits where a stream's queue is full */
+    st = g_calls[which].fn(v);
+    Py_END_ALLOW_THREADS
     if (st != HFQ_OK) {
         PyObject *e = Py_BuildValue("(is)", (int)st, hfq_last_error());
         if (e) {

@@ -282,3 +282,16 @@ def test_captured_call_and_another_stream(eo):
     c.quantless = c.xq, c.xq
     c.xq = None
     c.check()
+
+
+def test_a_rules_weights_belong_to_the_current_device(eo, monkeypatch):
+    c = Case(eo, 4, 256).call().check()
+    rule = eo.NormRule(None, c.w_pre, eo.HFQ_BF16)
+    eo.moe_norm_residual(rule, 4, 256, c.x, eo.HFQ_BF16, xn=c.xn)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)      # as if another were current
+    with pytest.raises(eo.HfqError, match="w_pre"):
+        rule_call = dict(x_dtype=eo.HFQ_BF16, xn=c.xn, stream=torch.cuda.default_stream(0))
+        eo.moe_norm_residual(rule, 4, 256, c.x, **rule_call)
+    monkeypatch.undo()
+    with pytest.raises(eo.HfqError, match="w_pre"):
+        eo.moe_norm_residual(eo.NormRule(None, c.w_pre.cpu(), eo.HFQ_BF16), 4, 256, c.x, eo.HFQ_BF16, xn=c.xn)
