@@ -295,10 +295,7 @@ cudaError_t launch_quantize(const void *x, bool bf16, size_t ldx, int rows, int 
 template <int TT, int R>
 cudaError_t launch_dot(const DotArgs &a, int smem, cudaStream_t s)
 {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(dot_kernel<TT, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
+    static_assert(2 * HFQ_Q8_MAX_K <= 48 * 1024, "two tokens' bytes need no leave");
     const int per = kDotWarps * R;
     return launch_ordered(dot_kernel<TT, R>, (a.m.N + per - 1) / per, kDotWarps * 32, smem, s, a);
 }

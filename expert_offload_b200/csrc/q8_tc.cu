@@ -122,7 +122,7 @@ __device__ bool wait_bar(uint64_t *bar, uint32_t parity, long long timeout_ns, v
 }
 
 // 32 consecutive columns of this thread's tensor-memory lane; they are there
-// after tmem_ld_wait().
+// after tmem_ld32_end(v), before which nothing may use them.
 __device__ __forceinline__ void tmem_ld32_begin(uint32_t taddr, int (&v)[32])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
@@ -136,10 +136,15 @@ __device__ __forceinline__ void tmem_ld32_begin(uint32_t taddr, int (&v)[32])
                  : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, int (&v)[32])
+// (The values pass through the wait, so that no use of them moves before it.)
+__device__ __forceinline__ void tmem_ld32_end(int (&v)[32])
 {
-    tmem_ld32_begin(taddr, v);
-    tmem_ld_wait();
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                   "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                   "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                   "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
 }
 
 __device__ __forceinline__ void store_y(const Q8Mat &m, int t, int n, float v)
@@ -404,11 +409,10 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
 #pragma unroll
                     for (int col = 0; col < C::kCols; col += 32) {
                         if (col >= tv) break;
-                        tmem_ld_wait();
-                        if (col + 32 < C::kCols) tmem_ld32_begin(trow + col + 32, v[(col / 32 + 1) & 1]);
+                        tmem_ld32_end(v[(col / 32) & 1]);
+                        if (col + 32 < C::kCols && col + 32 < tv) tmem_ld32_begin(trow + col + 32, v[(col / 32 + 1) & 1]);
                         store_columns(m, t0 + col, n, lane, pairs, ws, xs + col, v[(col / 32) & 1]);
                     }
-                    tmem_ld_wait();
                 } else {
                     // four tokens of a channel are 16 bytes, next to those of the next
                     // channel: a warp's store is one run of 512 bytes for each owner
@@ -418,7 +422,8 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
 #pragma unroll 1
                     for (int col = 0; col < tv; col += 32) {
                         int v[32];
-                        tmem_ld32(trow + col, v);
+                        tmem_ld32_begin(trow + col, v);
+                        tmem_ld32_end(v);
 #pragma unroll
                         for (int j = 0; j < 32; j += 4)
                             if (col + j < tv)
@@ -644,7 +649,7 @@ q8_pair_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
             tmem_ld32_begin(src, v[0]);
 #pragma unroll
             for (int j = 0; j < kPart / 32; ++j) {
-                tmem_ld_wait();
+                tmem_ld32_end(v[j & 1]);
                 if (j + 1 < kPart / 32) tmem_ld32_begin(src + 32 * (j + 1), v[(j + 1) & 1]);
                 else {                                       // this warp's last read of the buffer is done
                     tc_fence_before_sync();

@@ -5,7 +5,7 @@
 //   scale = RN_f32(amax / 127).
 //
 // The quotient is taken in f32 with one correction, u = u0 + (p - u0 amax) inv
-// with p = RN(v * 127), u0 = p * inv, inv = 1 / amax to 1 ulp: u is the exact
+// with p = RN(v * 127), u0 = p * inv, inv = 1 / amax to 2 ulp: u is the exact
 // p / amax but for one rounding.  Its nearest integer comes out of the low
 // bits of u + 1.5 * 2^23, half to even.
 //
