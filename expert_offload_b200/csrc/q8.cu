@@ -302,15 +302,17 @@ cudaError_t launch_dot(const DotArgs &a, int smem, cudaStream_t s)
 
 // One or two tokens and few weights: the dot kernel's short start wins (2.8
 // and 3.8 us for one and two tokens of 2048 x 1024, where the fused kernel takes
-// 4.8); with more of either the tensor cores' stream of weights does (17 us
+// 4.7); with more of either the tensor cores' stream of weights does (17 us
 // against 28 at 8192 x 8192).
 bool takes_dot(int T, int K, int N) { return T <= 2 && (long long)K * N * T <= (4 << 20); }
 
 // Up to eight tokens and few weights: the fused kernel, one launch (and 2 us of
 // host time) less.  With more weights the quantiser's own kernel, beside which
 // the product starts its weights, is quicker on the GPU (16.9 against 19.0 us for
-// 5 tokens of 8192 x 8192; 7.1 against 7.2 of 2048 x 8192).
-bool takes_fused(int T, int K, int N) { return T <= kQ8FusedTokens && (long long)K * N <= (16 << 20); }
+// 5 tokens of 8192 x 8192; 7.0 against 6.9 of 2048 x 8192), and with long rows,
+// which one warp a token quantises slowly (8192 x 2048: 7.5 against 8.3, 16384 x
+// 1024: 10.1 and 11.7; 4096 x 4096: 7.4 both; 2000 x 4096: 6.8 and 5.9).
+bool takes_fused(int T, int K, int N) { return T <= kQ8FusedTokens && K <= 4096 && (long long)K * N <= (16 << 20); }
 
 hfq_status run_dot(const DotArgs &a, cudaStream_t s)
 {

@@ -215,9 +215,8 @@ __device__ __forceinline__ void store_columns(const Q8Mat &m, int t0, int n, int
 // cluster), and write the CTA's share of the quantised rows where the MMAs read
 // them, in the 128-byte swizzle that a TMA load would have given them.  One
 // launch; x is read from L2 by every channel tile.  5 tokens of 2048 x 1024 take
-// 5.0 us, of 2048 x 8192 (17 MB of weights, 2.6 us) 7.2.
+// 4.7 us, of 2048 x 8192 (17 MB of weights, 2.6 us) 6.9.
 constexpr int kFew = 16;                  // tokens of its tile
-constexpr int kShare = 24;                // its stages of K: 48 KB of quantised tokens
 constexpr int kQuantWarps = 8;
 
 enum { kPlain = 0, kFusedBf16 = 1, kFusedF32 = 2 };
@@ -772,7 +771,6 @@ hfq_status launch_q8_fused(const Q8Mat &m, const void *x, bool x_bf16, size_t ld
     a.hook = option_take_extra_arrivals();
     const int nk = (m.K + kKb - 1) / kKb;
     a.split = split_of(kFew, (m.N + kCh - 1) / kCh, nk);
-    while ((nk + a.split - 1) / a.split > kShare) a.split *= 2;      // at most 128 stages: 8
     CUtensorMap wmap;
     if (!encode(&wmap, m.wq, m.K, m.N, m.ldw, kCh))
         return fail(HFQ_ERR_CUDA, "8-bit product: tensor map encoding failed (K %d, N %d)", m.K, m.N);
