@@ -303,8 +303,14 @@ cudaError_t launch_dot(const DotArgs &a, int smem, cudaStream_t s)
 // One or two tokens and few weights: the dot kernel's short start wins (2.8
 // and 3.8 us for one and two tokens of 2048 x 1024, where the fused kernel takes
 // 4.7); with more of either the tensor cores' stream of weights does (17 us
-// against 28 at 8192 x 8192).
-bool takes_dot(int T, int K, int N) { return T <= 2 && (long long)K * N * T <= (4 << 20); }
+// against 28 at 8192 x 8192).  Every block quantises its tokens whole, which
+// long rows make slow: one token of 4096 x 1024 takes 4.1 us (fused 5.3), of 8192
+// x 256 6.7 (6.8), of 16384 x 256 12.0 (9.5); two of 2048 x 256 3.7 (4.4), of 4096
+// x 128 5.6 (5.0).
+bool takes_dot(int T, int K, int N)
+{
+    return T <= 2 && K <= (T == 1 ? 8192 : 2048) && (long long)K * N * T <= (4 << 20);
+}
 
 // Up to eight tokens and few weights: the fused kernel, one launch (and 2 us of
 // host time) less.  With more weights the quantiser's own kernel, beside which

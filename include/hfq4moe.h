@@ -311,7 +311,7 @@ hfq_status moe_norm_residual(const moe_norm_rule *rule, int T, int H, const void
  *   y:      [T][N] in y_dtype, rows ldy elements apart (0 = N; else >= N).
  *
  * q8_linear: y = q8_matmul(q8_quantize_rows(x), wq): the same bits as the two
- * calls, in one launch where the tokens are few.
+ * calls, in one launch where the tokens and the weights are few.
  *   workspace: q8_linear_workspace_bytes(T, K, N) bytes of device scratch
  *           (may be NULL when that is 0), 256-byte aligned, with any contents;
  *           nothing in it is kept between calls, and calls that share it must

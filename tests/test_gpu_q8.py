@@ -193,6 +193,14 @@ def test_linear_large(eo, T, K, N, x, y):
     _both(eo, T, K, N, x, y)
 
 
+@pytest.mark.parametrize("T,K,N", [(1, 8192, 100), (1, 8193, 100), (2, 2048, 900), (2, 2049, 900), (8, 4096, 500),
+                                   (8, 4097, 500), (5, 8192, 2048), (8, 16384, 130), (33, 2048, 1024),
+                                   (33, 2049, 1024), (290, 1030, 1000), (600, 2048, 333), (1100, 300, 260)])
+@pytest.mark.parametrize("x,y", [("bf16", "f32"), ("f32", "bf16")])
+def test_linear_where_the_kernels_meet(eo, T, K, N, x, y):
+    _both(eo, T, K, N, x, y)
+
+
 @pytest.mark.parametrize("T", [1, 7, 40, 150, 700])
 @pytest.mark.parametrize("K,N,ldx,ldw,ldy,shift", [(300, 200, 301, 320, 203, 1), (512, 384, 520, 1024, 400, 0),
                                                    (1000, 1001, 1000, 1008, 1001, 3), (64, 8, 64, 64, 8, 4)])
