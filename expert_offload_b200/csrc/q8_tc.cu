@@ -147,13 +147,6 @@ __device__ __forceinline__ void tmem_ld32_end(int (&v)[32])
                    "+r"(v[29]), "+r"(v[30]), "+r"(v[31])::"memory");
 }
 
-__device__ __forceinline__ void store_y(const Q8Mat &m, int t, int n, float v)
-{
-    const size_t at = (size_t)t * m.ldy + n;
-    if (m.y_bf16) static_cast<uint16_t *>(m.y)[at] = float_to_bf16_bits(v);
-    else static_cast<float *>(m.y)[at] = v;
-}
-
 // Writes 32 columns of a warp: lane's channel n (ws its scale), tokens t0 ..
 // t0 + 31 (xs: their scales, shared memory).  All values first, then the
 // stores, those without a condition where the whole block lies inside: the
@@ -463,9 +456,22 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
                 sum[0] += p.x, sum[1] += p.y, sum[2] += p.z, sum[3] += p.w;
             }
             const float ws = ws_own[c];
+            float f[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (4 * q + j < tv) store_y(m, t0 + 4 * q + j, n, q8_value(sum[j], xs_own[4 * q + j], ws));
+            for (int j = 0; j < 4; ++j) f[j] = q8_value(sum[j], xs_own[4 * q + j], ws);
+            const int rows = tv - 4 * q;
+            const size_t at = (size_t)(t0 + 4 * q) * m.ldy + n;
+            if (m.y_bf16) {
+                uint16_t *p = static_cast<uint16_t *>(m.y) + at;
+#pragma unroll
+                for (int j = 0; j < 4; ++j, p += m.ldy)
+                    if (j < rows) *p = float_to_bf16_bits(f[j]);
+            } else {
+                float *p = static_cast<float *>(m.y) + at;
+#pragma unroll
+                for (int j = 0; j < 4; ++j, p += m.ldy)
+                    if (j < rows) *p = f[j];
+            }
         }
     }
     tc_fence_before_sync();
