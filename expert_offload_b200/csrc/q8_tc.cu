@@ -220,7 +220,7 @@ __device__ __forceinline__ void store_columns(const Q8Mat &m, int t0, int n, int
 // cluster), and write the CTA's share of the quantised rows where the MMAs read
 // them, in the 128-byte swizzle that a TMA load would have given them.  One
 // launch; x is read from L2 by every channel tile.  5 tokens of 2048 x 1024 take
-// 4.7 us, of 2048 x 8192 (17 MB of weights, 2.6 us) 6.9.
+// 4.5 us, of 2048 x 8192 (17 MB of weights, 2.6 us) 6.7.
 constexpr int kFew = 16;                  // tokens of its tile
 constexpr int kQuantWarps = 8;
 
@@ -451,10 +451,12 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
             const int q = i / own, c = i - q * own, n = n0 + rank * own + c;
             if (n >= m.N) continue;
             int sum[4] = {0, 0, 0, 0};
-            for (int r = 0; r < a.split; ++r) {
-                const int4 p = part[r * own * (BT / 4) + i];
-                sum[0] += p.x, sum[1] += p.y, sum[2] += p.z, sum[3] += p.w;
-            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r)                  // all requested before any is added
+                if (r < a.split) {
+                    const int4 p = part[r * own * (BT / 4) + i];
+                    sum[0] += p.x, sum[1] += p.y, sum[2] += p.z, sum[3] += p.w;
+                }
             const float ws = ws_own[c];
             float f[4];
 #pragma unroll
