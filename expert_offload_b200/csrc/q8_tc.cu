@@ -765,17 +765,19 @@ cudaError_t launch_pair(const Args &a, const CUtensorMap &wmap, const CUtensorMa
 // CTAs of a cluster for tiles of bt tokens.  Splitting K shortens each CTA's
 // run through it (0.27 us a stage) and puts more of the memory system to work,
 // up to two CTAs on an SM; it costs the exchange of the sums (about 1.5 us for
-// 64 tokens), so a tile of more than 16 tokens is split only if K is long enough.  Tokens x K x
-// N, one tile of K a CTA against the split: with tiles on most SMs 16 stages
-// lose (128 x 2048 x 8192: 11.4 us and 12.1), 64 gain (512 x 8192 x 2048: 28.7
-// and 23.8); with few tiles 4 stages lose (256 x 512 x 2048: 6.8 and 8.6), 16
-// gain (256 x 2048 x 1024: 11.2 and 9.0).
+// 64 tokens), so a tile of more than 16 tokens is split only if K is long enough.
+// Tokens x K x N, one tile of K a CTA against the split: with tiles on most SMs
+// 16 stages lose (128 x 2048 x 8192: 9.8 us and 10.5), 64 gain (512 x 8192 x 2048:
+// 26.6 and 22.1); with few tiles 4 stages lose (256 x 512 x 2048: 4.9 and 7.1), 16
+// gain (256 x 2048 x 1024: 8.9 and 7.3).  Eight CTAs of which some share SMs want
+// a longer K than four (16 x 2048 x 4096: 6.7 us with eight, 5.7 with four; 64 x
+// 4096 x 4096: 9.1 and 8.7; 16 x 8192 x 4096: 9.7 and 11.0).
 static int split_of(int bt, int tiles, int nk)
 {
-    const int sms = sm_count(), least = bt == kFew ? 1 : 2;
+    const int sms = sm_count(), least = bt == kFew ? 1 : 2, most = nk < 64 && 8 * tiles > sms ? 4 : 8;
     if (bt > kFew && nk < (bt > 32 && 2 * tiles > sms ? 32 : 8)) return 1;
     int split = 1;
-    while (split < 8 && nk >= 2 * split * least && tiles * split * 2 <= 2 * sms) split *= 2;
+    while (split < most && nk >= 2 * split * least && tiles * split * 2 <= 2 * sms) split *= 2;
     return split;
 }
 
@@ -809,12 +811,11 @@ hfq_status launch_q8_tc(const Q8Mat &m, bool chained, cudaStream_t s)
     a.chained = chained;
     a.hook = option_take_extra_arrivals();
     // Tiles of 16 and 32 tokens where they take all of them.  For more, CTA pairs
-    // once their 256 x 256 tiles fill most of the SMs (35.5 us against 37.9 with
+    // once their 256 x 256 tiles fill most of the SMs (32.4 us against 37.6 with
     // tiles of 128 at 512 x 8192 x 8192); else tiles of 32 while K is short and
     // they need half of the SMs at most, since the epilogue is then most of the
-    // time (256 x 2048 x 1024: 7.7 us against 9.2 with tiles of 64, 128 x 1024 x
-    // 1024: 6.0 and 6.8; of the shapes timed, only 40 x 2048 x 2048 lost: 7.1 and
-    // 6.4); else tiles of 64 as long as there are no more than two for each SM,
+    // time (128 x 1024 x 1024: 5.7 us against 6.3 with tiles of 64, 40 x 2048 x
+    // 2048: 6.2 and 6.4); else tiles of 64 as long as there are no more than two for each SM,
     // else of 128.
     const int sms = sm_count(), nk = (m.K + kKb - 1) / kKb;
     const int ct = (m.N + kCh - 1) / kCh, pairs = (m.N + 2 * kCh - 1) / (2 * kCh) * ((m.T + 255) / 256);
