@@ -16,23 +16,23 @@ struct QuantArgs {
     int8_t *q;
     float *scale;
     size_t ldx, ldq;
-    int rows, cols, bf16, swiglu, vec;
+    int rows, cols;
     int per_row;                 // threads of a row, a power of two of at least 32
 };
 
 // A row is read once: `per_row` threads hold it in registers, NV chunks of 8
 // each, between the maximum and the bytes.  Bound by memory (3 bytes an
 // element of a bf16 row), so everything is requested before anything is used
-// and held as it came (VEC: rows of whole 16-byte pieces): 8192 rows of 8192 in
-// bf16 take 41.7 us (31 at the rate of a copy), in f32 55.3 (52).
-template <bool EXACT>            // values of bf16
-__device__ __forceinline__ void write_row(const QuantArgs &a, size_t r, int j, int i, const float (&v)[8],
-                                          const RowQuant<EXACT> &q)
+// and held as it came (rows of whole 16-byte pieces): 8192 rows of 8192 in bf16
+// take 41.2 us (31 at the rate of a copy), in f32 55.3 (52).  SwiGLU's
+// exponentials bound by instructions: 8192 rows of 2 x 2048 in bf16 take 25.4 us
+// (13 at the rate of a copy), in f32 26.4 (23).
+
+// Chunk i of thread j (`q`: its bytes, zeros behind the row).
+__device__ __forceinline__ void write_row(const QuantArgs &a, size_t r, int j, int i, uint2 q)
 {
     const int c = (i * a.per_row + j) * 8;
-    int8_t *out = a.q + r * a.ldq + c;
-    if (c < a.cols) *reinterpret_cast<uint2 *>(out) = q(v);
-    else if (c < (int)round16(a.cols)) *reinterpret_cast<uint2 *>(out) = make_uint2(0u, 0u);
+    if (c < (int)round16(a.cols)) *reinterpret_cast<uint2 *>(a.q + r * a.ldq + c) = q;
 }
 
 // The largest magnitude of a row, from its threads'.
@@ -49,8 +49,16 @@ __device__ __forceinline__ uint32_t row_top(const QuantArgs &a, uint32_t top, ui
     return top;
 }
 
-template <int NV, bool BF16>
-__global__ void __launch_bounds__(512, 2) quantize_vec_kernel(QuantArgs a)
+// silu(g) * u: expf within 2 ulp, the reciprocal within 1 (of 1 + inf: 0).
+__device__ __forceinline__ float swiglu(float g, float u)
+{
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + expf(-g)));
+    return g * r * u;
+}
+
+template <int NV, bool BF16, bool SWIGLU>
+__global__ void __launch_bounds__(512, SWIGLU && NV > 2 ? 1 : 2) quantize_vec_kernel(QuantArgs a)
 {
     __shared__ uint32_t red[16];
     begin_ordered();
@@ -58,52 +66,77 @@ __global__ void __launch_bounds__(512, 2) quantize_vec_kernel(QuantArgs a)
     const size_t r = (size_t)blockIdx.x * (blockDim.x / a.per_row) + threadIdx.x / a.per_row;
     const bool in = r < (size_t)a.rows;
     const void *row = row_at(a.x, BF16, in ? r * a.ldx : 0);
-    Raw8 raw[NV];
+    Raw8 raw[NV], up[SWIGLU ? NV : 1];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = (i * a.per_row + j) * 8;
         raw[i].a = raw[i].b = make_uint4(0u, 0u, 0u, 0u);
-        if (in && c < a.cols) raw[i] = load_raw8<BF16>(row, c);
+        if (SWIGLU) up[i] = raw[i];
+        if (in && c < a.cols) {
+            raw[i] = load_raw8<BF16>(row, c);
+            if (SWIGLU) up[i] = load_raw8<BF16>(row, a.cols + c);
+        }
     }
     uint32_t top = 0;
+    float v[SWIGLU ? NV : 1][8];
+    if (SWIGLU) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) top = max(top, raw_max<BF16>(raw[i]));
+        for (int i = 0; i < NV; ++i) {
+            float u[8];
+            expand8<BF16>(raw[i], v[i]);
+            expand8<BF16>(up[i], u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[i][e] = swiglu(v[i][e], u[e]);
+                top = max(top, abs_bits(v[i][e]));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) top = max(top, raw_max<BF16>(raw[i]));
+    }
     top = row_top(a, top, red);
     if (!in) return;
-    const RowQuant<BF16> q(top);
+    const RowQuant<BF16 && !SWIGLU> q(top);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        float v[8];
-        expand8<BF16>(raw[i], v);
-        write_row<BF16>(a, r, j, i, v, q);
+        if (!SWIGLU) expand8<BF16>(raw[i], v[0]);
+        write_row(a, r, j, i, q(v[SWIGLU ? i : 0]));
     }
     if (j == 0) a.scale[r] = row_scale(top);
 }
 
-template <int NV, bool EXACT>
+// Rows of any length and alignment: neighbouring threads read neighbouring
+// elements, and the bytes change places in shared memory.  517 rows of 2001 in
+// f32 take 2.8 us (3.6 with threads of eight neighbours each), 8192 of 8001 66.6
+// (73.2); in bf16 2.5 (2.8) and, bound by their 2-byte loads, 91.8 (84.1).
+template <int NV, bool BF16, bool SWIGLU>
 __global__ void __launch_bounds__(512) quantize_kernel(QuantArgs a)
 {
     __shared__ uint32_t red[16];
+    __shared__ __align__(16) uint8_t bytes[512 * NV * 8];
     begin_ordered();
-    const int j = threadIdx.x & (a.per_row - 1);
-    const size_t r = (size_t)blockIdx.x * (blockDim.x / a.per_row) + threadIdx.x / a.per_row;
+    const int sub = threadIdx.x / a.per_row, j = threadIdx.x & (a.per_row - 1);
+    const size_t r = (size_t)blockIdx.x * (blockDim.x / a.per_row) + sub;
     const bool in = r < (size_t)a.rows;
-    const void *row = row_at(a.x, a.bf16, in ? r * a.ldx : 0);
-    float v[NV][8];
+    const void *row = row_at(a.x, BF16, in ? r * a.ldx : 0);
+    const int n = in ? a.cols : 0;
+    auto read = [&](int c) { return c < n ? load_act(row, BF16 ? HFQ_BF16 : HFQ_F32, c) : 0.0f; };
+    float v[NV][8], u[SWIGLU ? NV : 1][8];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = (i * a.per_row + j) * 8;
-        load8(row, a.bf16, a.vec, c, in ? a.cols : 0, v[i]);
-    }
-    if (!EXACT && a.swiglu) {
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * a.per_row + j) * 8;
-            float u[8];
-            load8(row_at(row, a.bf16, a.cols), a.bf16, a.vec, c, in ? a.cols : 0, u);
+        for (int e = 0; e < 8; ++e) v[i][e] = read((i * 8 + e) * a.per_row + j);
+    if (SWIGLU) {
+        row = row_at(row, BF16, a.cols);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[i][e] = v[i][e] / (1.0f + expf(-v[i][e])) * u[e];
-        }
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[i][e] = read((i * 8 + e) * a.per_row + j);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[i][e] = swiglu(v[i][e], u[i][e]);
     }
     uint32_t top = 0;
 #pragma unroll
@@ -111,11 +144,26 @@ __global__ void __launch_bounds__(512) quantize_kernel(QuantArgs a)
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = max(top, abs_bits(v[i][e]));
     top = row_top(a, top, red);
-    if (!in) return;
-    const RowQuant<EXACT> q(top);
+    const RowQuant<BF16 && !SWIGLU> q(top);
+    uint8_t *mine = bytes + sub * a.per_row * NV * 8;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) write_row<EXACT>(a, r, j, i, v[i], q);
+    for (int i = 0; i < NV; ++i) {
+        const uint2 b = q(v[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mine[(i * 8 + e) * a.per_row + j] = (uint8_t)((e < 4 ? b.x : b.y) >> 8 * (e & 3));
+    }
+    __syncthreads();
+    if (!in) return;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) write_row(a, r, j, i, *reinterpret_cast<const uint2 *>(mine + (i * a.per_row + j) * 8));
     if (j == 0) a.scale[r] = row_scale(top);
+}
+
+template <bool BF16, bool SWIGLU>
+void (*quantizer(bool vec, int nv))(QuantArgs)
+{
+    if (vec) return nv == 2 ? quantize_vec_kernel<2, BF16, SWIGLU> : quantize_vec_kernel<4, BF16, SWIGLU>;
+    return nv == 2 ? quantize_kernel<2, BF16, SWIGLU> : quantize_kernel<4, BF16, SWIGLU>;
 }
 
 // -------------------------------------------------- few tokens: dot products
@@ -276,19 +324,15 @@ hfq_status check_out(const char *who, int T, int K, const int8_t *wq, int ldw, c
 cudaError_t launch_quantize(const void *x, bool bf16, size_t ldx, int rows, int cols, bool swiglu, int8_t *q, size_t ldq,
                             float *scale, cudaStream_t s)
 {
-    QuantArgs a{x, q, scale, ldx, ldq, rows, cols, bf16, swiglu, 0, 32};
+    QuantArgs a{x, q, scale, ldx, ldq, rows, cols, 32};
     const size_t size = bf16 ? 2 : 4;
     // rows at 16-byte addresses, of whole 8-element pieces
-    a.vec = aligned16(x) && ldx * size % 16 == 0 && cols % 8 == 0;
+    const bool vec = aligned16(x) && ldx * size % 16 == 0 && cols % 8 == 0;
     const int nv = cols <= 4096 ? 2 : 4;
     while (a.per_row * 8 * nv < cols) a.per_row *= 2;      // at most 512
     const int block = std::max(a.per_row, 256), per = block / a.per_row, grid = (rows + per - 1) / per;
-    void (*kernel)(QuantArgs);
-    if (a.vec && !swiglu)
-        kernel = nv == 2 ? (bf16 ? quantize_vec_kernel<2, true> : quantize_vec_kernel<2, false>)
-                         : (bf16 ? quantize_vec_kernel<4, true> : quantize_vec_kernel<4, false>);
-    else if (bf16 && !swiglu) kernel = nv == 2 ? quantize_kernel<2, true> : quantize_kernel<4, true>;
-    else kernel = nv == 2 ? quantize_kernel<2, false> : quantize_kernel<4, false>;
+    void (*kernel)(QuantArgs) = bf16 ? (swiglu ? quantizer<true, true>(vec, nv) : quantizer<true, false>(vec, nv))
+                                     : (swiglu ? quantizer<false, true>(vec, nv) : quantizer<false, false>(vec, nv));
     return launch_ordered(kernel, grid, block, 0, s, a);
 }
 

@@ -119,6 +119,21 @@ def test_quantiser_strides(eo, rows, cols, ldx, ldq, shift, kind):
     np.testing.assert_array_equal(s.cpu().numpy(), rs)
 
 
+@pytest.mark.parametrize("rows,cols,ldx,shift", [(9, 512, 1030, 0), (7, 520, 1048, 8), (70, 4096, 8192, 1),
+                                                 (3, 4097, 8200, 0), (2, 16383, 32766, 3), (600, 1, 2, 0)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_swiglu_quantiser_strides(eo, rows, cols, ldx, shift, kind):
+    """The bytes do not hang on how a row lies: those of the same rows, dense and
+    aligned where their length allows it."""
+    base = _randn(rows + cols, rows * ldx + shift, dt=kind)[shift:]
+    q, s = _quantise(eo, base, rows, cols, kind, act=eo.ACT_SWIGLU, ldx=ldx)
+    dense = base[:rows * ldx].view(rows, ldx)[:, :2 * cols].contiguous()
+    q2, s2 = _quantise(eo, dense, rows, cols, kind, act=eo.ACT_SWIGLU)
+    assert torch.equal(q, q2) and torch.equal(s, s2)
+    v = q8.swiglu(dense.float().cpu().numpy())
+    assert np.all(np.abs(s.double().cpu().numpy() - np.abs(v).max(1) / 127) <= 11 * U * np.abs(v).max(1) / 127)
+
+
 @pytest.mark.parametrize("rows,cols", [(1, 512), (5, 96), (3, 1001), (2, 16384)])
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 def test_swiglu_quantiser(eo, rows, cols, kind):
