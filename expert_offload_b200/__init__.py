@@ -154,7 +154,9 @@ def _ptr(a):
     raise TypeError(f"cannot take the address of {type(a)}")
 
 
-def _nbytes(a) -> int:
+def _nbytes(a, name: str = "workspace") -> int:
+    if isinstance(a, int):
+        raise HfqError(-1, f"{name} must be a tensor or an array: an address does not say its size")
     if hasattr(a, "nbytes") and not callable(a.nbytes):
         return int(a.nbytes)
     return int(a.numel() * a.element_size())
@@ -165,12 +167,41 @@ _ROUTE, _NORM, _QUANTIZE, _MATMUL, _LINEAR = range(5)
 _call = None
 
 
-def _strided(name, t, n) -> None:
-    """The checks of an operand that is not simply dense and large enough."""
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise HfqError(-1, f"{name}: the elements of a row are not next to each other")
-    if t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() < n:
-        raise HfqError(-1, f"{name} holds fewer than the {n} elements the call reads or writes")
+def _dense(name, t, n) -> None:
+    """n elements without a gap."""
+    if not t.is_contiguous():
+        raise HfqError(-1, f"{name} has gaps between its elements, which the call takes as neighbours")
+    if t.numel() < n:
+        raise HfqError(-1, f"{name} holds fewer elements than the call reads or writes")
+
+
+def _layout(name, t, rows, cols, ld, whole) -> None:
+    """Rows of cols elements that start ld apart, in a tensor that is not exactly
+    rows * ld elements without a gap.  A row is what some of the last dimensions
+    hold without a gap; all others count rows.  A flat buffer has no rows of its
+    own, and one row has no distance."""
+    dims = [(n, s) for n, s in zip(t.shape, t.stride()) if n != 1]
+    have, at = 1, len(dims)              # elements of a row, from dimension `at` on
+    while at and dims[at - 1][1] == have and have < ld:
+        at -= 1
+        have *= dims[at][0]
+    if at == 0:                          # without a gap up to ld or the tensor's end
+        flat = len(dims) <= 1 or rows == 1 or have == ld
+        ok = flat and have >= (rows - 1) * ld + cols
+    elif rows == 1:
+        ok = have >= cols
+    else:
+        count, step = 1, ld
+        for n, s in reversed(dims[:at]):
+            if s != step:
+                break
+            count, step = count * n, step * n
+        ok = have >= cols and have <= ld and count >= rows
+    if not ok:
+        raise HfqError(-1, f"{name} does not hold {rows} rows of {cols} elements that start {ld} apart")
+    if whole > cols and (t.untyped_storage().nbytes() // t.element_size() - t.storage_offset() <
+                         (rows - 1) * ld + whole):
+        raise HfqError(-1, f"{name} needs {whole} elements of memory for its last row")
 
 
 def _bind(*args) -> None:
@@ -185,9 +216,9 @@ def _bind(*args) -> None:
     spec.loader.exec_module(mod)
     torch = sys.modules.get("torch")
     if torch is None:
-        mod.setup(HfqError, _strided, None, None, {})
+        mod.setup(HfqError, _layout, None, None, {})
     else:
-        mod.setup(HfqError, _strided, torch.Tensor, torch._C._cuda_getDevice if torch.cuda.is_available() else None,
+        mod.setup(HfqError, _layout, torch.Tensor, torch._C._cuda_getDevice if torch.cuda.is_available() else None,
                   {HFQ_F32: (torch.float32,), HFQ_BF16: (torch.bfloat16, torch.int16, torch.uint16),
                    _I32: (torch.int32,), _I8: (torch.int8,),
                    _ANY: (torch.uint8, torch.int8, torch.int16, torch.int32, torch.int64, torch.float32)})
@@ -225,13 +256,13 @@ def hfq4_expert_bytes(hidden: int, inter: int) -> int:
 def hfq4_pack_experts(gate, up, down, out, n_experts: int, hidden: int, inter: int) -> None:
     """Host packer: numpy f32 gate/up [E,I,H], down [E,H,I] -> out uint8 bytes."""
     _check(lib().hfq4_pack_experts(_ptr(gate), _ptr(up), _ptr(down), n_experts, hidden, inter,
-                                   _ptr(out), _nbytes(out)))
+                                   _ptr(out), _nbytes(out, "out")))
 
 
 def hfq4_pack_experts_device(gate, up, down, out, n_experts: int, hidden: int, inter: int,
                              stream=None) -> None:
     _check(lib().hfq4_pack_experts_device(_ptr(gate), _ptr(up), _ptr(down), n_experts, hidden,
-                                          inter, _ptr(out), _nbytes(out), _stream(stream)))
+                                          inter, _ptr(out), _nbytes(out, "out"), _stream(stream)))
 
 
 def hfq4_dequant(blocks, rows: int, cols: int, out, stream=None) -> None:
@@ -275,13 +306,13 @@ def moe_route_scored(logits, logits_dtype: int, T: int, E: int, k: int, rule: Ro
                      bias=None, cnt=None, off=None, perm=None, workspace=None, ld: int = 0,
                      stream=None) -> None:
     """Top-k routing by scores and a bias, with groups; lists as moe_route's."""
-    (_call or _bind)(_ROUTE, ("logits", logits, logits_dtype, (T - 1) * (ld or E) + E), logits_dtype, ld, T, E,
-                     bias if bias is None else ("bias", bias, HFQ_F32, E), rule.address, k,
-                     ("idx", idx, _I32, T * k), ("wts", wts, HFQ_F32, T * k),
-                     cnt if cnt is None else ("cnt", cnt, _I32, E),
-                     off if off is None else ("off", off, _I32, E + 1),
-                     perm if perm is None else ("perm", perm, _I32, T * k),
-                     workspace if workspace is None else ("workspace", workspace, _ANY, 0),
+    (_call or _bind)(_ROUTE, ("logits", logits, logits_dtype, T, E, ld or E, E), logits_dtype, ld, T, E,
+                     bias if bias is None else ("bias", bias, HFQ_F32, 1, E), rule.address, k,
+                     ("idx", idx, _I32, T, k), ("wts", wts, HFQ_F32, T, k),
+                     cnt if cnt is None else ("cnt", cnt, _I32, 1, E),
+                     off if off is None else ("off", off, _I32, 1, E + 1),
+                     perm if perm is None else ("perm", perm, _I32, T, k),
+                     workspace if workspace is None else ("workspace", workspace, _ANY, 0, 0),
                      0 if workspace is None else _nbytes(workspace), _stream(stream))
 
 
@@ -312,7 +343,7 @@ class NormRule:
             kinds = (torch.float32,) if self.w_dtype == HFQ_F32 else (torch.bfloat16, torch.int16, torch.uint16)
             if not w.is_cuda or w.get_device() != torch._C._cuda_getDevice() or w.dtype not in kinds:
                 raise HfqError(-1, f"{name} is not a tensor of the current CUDA device of the rule's w_dtype")
-            _strided(name, w, H)
+            _dense(name, w, H)
             self.device = w.get_device()
         self.checked = H
 
@@ -323,17 +354,17 @@ def moe_norm_residual(rule: NormRule, T: int, H: int, x, x_dtype: int, y=None, y
     """x' = residual_scale x + branch_scale gate norm(y + y2), xn = norm(x')."""
     if rule.tensors and (rule.checked < H or rule.device != sys.modules["torch"]._C._cuda_getDevice()):
         rule.check(H)
-    nx, ny = (T - 1) * (ldx or H) + H, (T - 1) * (ldy or H) + H
-    kind = rule.gate_kind
-    (_call or _bind)(_NORM, rule.address, T, H, ("x", x, x_dtype, nx), x_dtype, ldx,
-                     y if y is None else ("y", y, y_dtype, ny), y2 if y2 is None else ("y2", y2, y_dtype, ny),
-                     y_dtype, ldy, y2_gate if y2_gate is None else ("y2_gate", y2_gate, HFQ_F32, T),
+    lx, ly, kind = ldx or H, ldy or H, rule.gate_kind
+    (_call or _bind)(_NORM, rule.address, T, H, ("x", x, x_dtype, T, H, lx, H), x_dtype, ldx,
+                     y if y is None else ("y", y, y_dtype, T, H, ly, H),
+                     y2 if y2 is None else ("y2", y2, y_dtype, T, H, ly, H), y_dtype, ldy,
+                     y2_gate if y2_gate is None else ("y2_gate", y2_gate, HFQ_F32, T, 1),
                      gate if gate is None else
-                     ("gate", gate, HFQ_F32, T if kind == GATE_TOKEN else H if kind == GATE_CHANNEL else T * H),
-                     x_out if x_out is None else ("x_out", x_out, x_dtype, nx),
-                     xn if xn is None else ("xn", xn, xn_dtype, T * H), xn_dtype,
-                     xq if xq is None else ("xq", xq, _I8, T * (-(-H // 16) * 16)),
-                     xq_scale if xq_scale is None else ("xq_scale", xq_scale, HFQ_F32, T), _stream(stream))
+                     ("gate", gate, HFQ_F32, 1 if kind == GATE_CHANNEL else T, 1 if kind == GATE_TOKEN else H),
+                     x_out if x_out is None else ("x_out", x_out, x_dtype, T, H, lx, H),
+                     xn if xn is None else ("xn", xn, xn_dtype, T, H), xn_dtype,
+                     xq if xq is None else ("xq", xq, _I8, T, -(-H // 16) * 16),
+                     xq_scale if xq_scale is None else ("xq_scale", xq_scale, HFQ_F32, T, 1), _stream(stream))
 
 
 # --------------------------------------------------- products in 8 bits
@@ -343,8 +374,8 @@ def q8_quantize_rows(x, x_dtype: int, rows: int, cols: int, q, scale, act: int =
     """int8 rows and their f32 scales; act ACT_SWIGLU quantises silu(gate) * up."""
     width = 2 * cols if act == ACT_SWIGLU else cols
     c16 = -(-cols // 16) * 16
-    (_call or _bind)(_QUANTIZE, ("x", x, x_dtype, (rows - 1) * (ldx or width) + width), x_dtype, ldx, rows, cols, act,
-                     ("q", q, _I8, (rows - 1) * (ldq or c16) + c16), ldq, ("scale", scale, HFQ_F32, rows),
+    (_call or _bind)(_QUANTIZE, ("x", x, x_dtype, rows, width, ldx or width, width), x_dtype, ldx, rows, cols, act,
+                     ("q", q, _I8, rows, c16, ldq or c16, c16), ldq, ("scale", scale, HFQ_F32, rows, 1),
                      _stream(stream))
 
 
@@ -352,9 +383,9 @@ def q8_matmul(xq, xs, T: int, K: int, wq, ws, N: int, y, y_dtype: int, ldxq: int
               ldy: int = 0, stream=None) -> None:
     """y = (xq wq^T) * xs * ws for quantised rows xq and channels wq."""
     k16 = -(-K // 16) * 16
-    (_call or _bind)(_MATMUL, ("xq", xq, _I8, (T - 1) * (ldxq or k16) + k16), ldxq, ("xs", xs, HFQ_F32, T), T, K,
-                     ("wq", wq, _I8, (N - 1) * (ldw or k16) + k16), ldw, ("ws", ws, HFQ_F32, N), N,
-                     ("y", y, y_dtype, (T - 1) * (ldy or N) + N), y_dtype, ldy, _stream(stream))
+    (_call or _bind)(_MATMUL, ("xq", xq, _I8, T, K, ldxq or k16, k16), ldxq, ("xs", xs, HFQ_F32, T, 1), T, K,
+                     ("wq", wq, _I8, N, K, ldw or k16, k16), ldw, ("ws", ws, HFQ_F32, N, 1), N,
+                     ("y", y, y_dtype, T, N, ldy or N, N), y_dtype, ldy, _stream(stream))
 
 
 def q8_linear_workspace_bytes(T: int, K: int, N: int) -> int:
@@ -365,10 +396,10 @@ def q8_linear(x, x_dtype: int, T: int, K: int, wq, ws, N: int, y, y_dtype: int, 
               ldw: int = 0, ldy: int = 0, stream=None) -> None:
     """y = x W^T with x quantised on the way: q8_quantize_rows, then q8_matmul."""
     k16 = -(-K // 16) * 16
-    (_call or _bind)(_LINEAR, ("x", x, x_dtype, (T - 1) * (ldx or K) + K), x_dtype, ldx, T, K,
-                     ("wq", wq, _I8, (N - 1) * (ldw or k16) + k16), ldw, ("ws", ws, HFQ_F32, N), N,
-                     ("y", y, y_dtype, (T - 1) * (ldy or N) + N), y_dtype, ldy,
-                     workspace if workspace is None else ("workspace", workspace, _ANY, 0),
+    (_call or _bind)(_LINEAR, ("x", x, x_dtype, T, K, ldx or K, K), x_dtype, ldx, T, K,
+                     ("wq", wq, _I8, N, K, ldw or k16, k16), ldw, ("ws", ws, HFQ_F32, N, 1), N,
+                     ("y", y, y_dtype, T, N, ldy or N, N), y_dtype, ldy,
+                     workspace if workspace is None else ("workspace", workspace, _ANY, 0, 0),
                      0 if workspace is None else _nbytes(workspace), _stream(stream))
 
 
@@ -516,7 +547,7 @@ class ExpertCache:
         h = ctypes.c_void_p()
         _check(lib().hfq_cache_create(L, E, expert_bytes, slots, self._keep[0].ctypes.data,
                                       self._keep[1].ctypes.data, self._keep[2].ctypes.data,
-                                      _ptr(slot_mem), _nbytes(slot_mem) if slot_mem is not None else 0,
+                                      _ptr(slot_mem), _nbytes(slot_mem, "slot_mem") if slot_mem is not None else 0,
                                       _ptr(table_dev), _ptr(loc_dev), _stream(stream), ctypes.byref(h)))
         self.handle = h.value
 

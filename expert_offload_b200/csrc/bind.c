@@ -5,10 +5,15 @@
  * Python took 7 us a call.
  *
  * call(index, arg, ...): an argument is a whole number, None (0) or an operand,
- * a tuple (name, tensor or address or None, kind, elements): a CUDA tensor of
- * the current device, of the kind's type, with at least that many elements, or
- * a raw device address, which is the caller's word.  A failed check or call
- * raises HfqError.
+ * a tuple of a name, a tensor or an address or None, a kind, and what the call
+ * reads or writes:
+ *   (name, t, kind, rows, cols): rows * cols elements without a gap;
+ *   (name, t, kind, rows, cols, ld, whole): rows of cols elements that start ld
+ *   elements apart, of which memory holds `whole` (what stands behind cols does
+ *   not count).
+ * A tensor is one of the current CUDA device and of the kind's type, and has
+ * those elements where the call expects them.  A raw device address is the
+ * caller's word.  A failed check or call raises HfqError.
  */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -20,7 +25,7 @@
 #define MAX_ARGS 24
 #define MAX_KINDS 8
 
-static PyObject *g_error, *g_tensor, *g_get_device, *g_slow, *g_kinds[MAX_KINDS];
+static PyObject *g_error, *g_tensor, *g_get_device, *g_layout, *g_kinds[MAX_KINDS];
 static PyObject *s_dtype, *s_get_device, *s_is_contiguous, *s_numel, *s_data_ptr;
 
 typedef int64_t V;
@@ -97,10 +102,21 @@ static int ask(PyObject *t, PyObject *method, V *v)
     return st;
 }
 
+static int out_of_range(void)
+{
+    PyObject *name = PyUnicode_FromString("a size");
+    if (name) {
+        fail_arg(name, "is out of range");
+        Py_DECREF(name);
+    }
+    return -1;
+}
+
 static int operand(PyObject *op, V *v, V *device)
 {
-    if (PyTuple_GET_SIZE(op) != 4) {
-        PyErr_SetString(PyExc_TypeError, "an operand is (name, tensor, kind, elements)");
+    const Py_ssize_t parts = PyTuple_GET_SIZE(op);
+    if (parts != 5 && parts != 7) {
+        PyErr_SetString(PyExc_TypeError, "an operand is (name, tensor, kind, rows, cols) or (.., rows, cols, ld, whole)");
         return -1;
     }
     PyObject *name = PyTuple_GET_ITEM(op, 0), *t = PyTuple_GET_ITEM(op, 1);
@@ -111,7 +127,7 @@ static int operand(PyObject *op, V *v, V *device)
     if (PyLong_Check(t)) return to_word(t, v);
     if (!g_tensor || !PyObject_TypeCheck(t, (PyTypeObject *)g_tensor))
         return fail_arg(name, "is neither a tensor of the current CUDA device nor a device address");
-    V on = -1, numel = 0, want = 0;
+    V on = -1, numel = 0, size[4] = {0, 0, 0, 0};        /* rows, cols, ld, whole */
     if (ask(t, s_get_device, &on)) return -1;
     if (on >= 0 && *device < 0) {
         PyObject *r = PyObject_CallNoArgs(g_get_device);
@@ -132,14 +148,24 @@ static int operand(PyObject *op, V *v, V *device)
             known |= PyTuple_GET_ITEM(g_kinds[kind], i) == dtype;
     Py_DECREF(dtype);
     if (!known) return fail_arg(name, "has another type than the call names");
+    for (Py_ssize_t i = 0; i < parts - 3; ++i) {
+        if (to_word(PyTuple_GET_ITEM(op, 3 + i), &size[i])) return -1;
+        if (size[i] < INT_MIN || size[i] > INT_MAX) return out_of_range();
+    }
     PyObject *dense = PyObject_CallMethodNoArgs(t, s_is_contiguous);
     if (!dense) return -1;
     const int is_dense = dense == Py_True;
     Py_DECREF(dense);
-    if (to_word(PyTuple_GET_ITEM(op, 3), &want)) return -1;
     if (ask(t, s_numel, &numel)) return -1;
-    if (!is_dense || numel < want) {             /* strided, or a view of a larger storage: in Python */
-        PyObject *r = PyObject_CallFunctionObjArgs(g_slow, name, t, PyTuple_GET_ITEM(op, 3), NULL);
+    const V rows = size[0], cols = size[1], ld = size[2], whole = size[3];
+    if (parts == 5) {
+        if (!is_dense) return fail_arg(name, "has gaps between its elements, which the call takes as neighbours");
+        if (rows > 0 && cols > 0 && numel < rows * cols)
+            return fail_arg(name, "holds fewer elements than the call reads or writes");
+    } else if (rows > 0 && cols > 0 && ld >= cols &&     /* else the library refuses the sizes */
+               !(is_dense && numel == rows * ld && whole <= ld)) {
+        PyObject *r = PyObject_CallFunction(g_layout, "OOLLLL", name, t, (long long)rows, (long long)cols, (long long)ld,
+                                            (long long)whole);
         if (!r) return -1;
         Py_DECREF(r);
     }
@@ -168,11 +194,7 @@ static PyObject *call(PyObject *self, PyObject *const *args, Py_ssize_t n)
             Py_DECREF(w);
             if (st) return NULL;
             if (g_calls[which].sig[i] == 'i' && (v[i] < INT_MIN || v[i] > INT_MAX)) {
-                PyObject *nm = PyUnicode_FromString("a size");
-                if (nm) {
-                    fail_arg(nm, "is out of range");
-                    Py_DECREF(nm);
-                }
+                out_of_range();
                 return NULL;
             }
         }
@@ -192,18 +214,18 @@ static PyObject *call(PyObject *self, PyObject *const *args, Py_ssize_t n)
     Py_RETURN_NONE;
 }
 
-/* setup(error, slow check, torch.Tensor or None, current device's call, {kind: (dtypes)}) */
+/* setup(error, check of a matrix' layout, torch.Tensor or None, current device's call, {kind: (dtypes)}) */
 static PyObject *setup(PyObject *self, PyObject *args)
 {
     (void)self;
-    PyObject *error, *slow, *tensor, *get_device, *kinds;
-    if (!PyArg_ParseTuple(args, "OOOOO!", &error, &slow, &tensor, &get_device, &PyDict_Type, &kinds)) return NULL;
+    PyObject *error, *layout, *tensor, *get_device, *kinds;
+    if (!PyArg_ParseTuple(args, "OOOOO!", &error, &layout, &tensor, &get_device, &PyDict_Type, &kinds)) return NULL;
     if (tensor != Py_None && !PyType_Check(tensor)) {
         PyErr_SetString(PyExc_TypeError, "setup: a tensor type or None");
         return NULL;
     }
     Py_XSETREF(g_error, Py_NewRef(error));
-    Py_XSETREF(g_slow, Py_NewRef(slow));
+    Py_XSETREF(g_layout, Py_NewRef(layout));
     Py_XSETREF(g_tensor, tensor == Py_None ? NULL : Py_NewRef(tensor));
     Py_XSETREF(g_get_device, Py_NewRef(get_device));
     PyObject *k, *d;
@@ -221,7 +243,7 @@ static PyObject *setup(PyObject *self, PyObject *args)
 
 static PyMethodDef methods[] = {
     {"call", (PyCFunction)(void (*)(void))call, METH_FASTCALL, "call(index, arguments): a checked call of the library"},
-    {"setup", setup, METH_VARARGS, "setup(error, slow, tensor, get_device, kinds)"},
+    {"setup", setup, METH_VARARGS, "setup(error, layout, tensor, get_device, kinds)"},
     {NULL, NULL, 0, NULL}};
 
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", NULL, -1, methods, NULL, NULL, NULL, NULL};
