@@ -7,6 +7,10 @@
 // successor begin (let_next_begin) only after that, so that whatever such a
 // kernel finds done is done for its successors, too.  Launches of other makers,
 // before and behind, are ordered as always.
+//
+// What its predecessors may still write while it is resident is not read-only
+// for the time that it runs, so such a kernel reads memory by plain loads, never
+// by __ldg or ld.global.nc, which ask for that.
 #pragma once
 
 #include <cuda_runtime.h>

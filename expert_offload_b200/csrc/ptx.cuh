@@ -203,6 +203,17 @@ __device__ __forceinline__ uint4 ld_nc_v4(const void *p)
     return v;
 }
 
+// Of memory that other kernels may write while this one is resident: the
+// volatile keeps the load behind the wait for them.
+__device__ __forceinline__ uint4 ld_v4(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 }  // namespace hfq
 
 namespace hfq {

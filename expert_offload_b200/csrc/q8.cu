@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kDotWarps * 32) dot_kernel(const DotArgs a)
     const int n0 = (blockIdx.x * kDotWarps + warp) * R;
     const int k16 = (int)round16(m.K), kp = (m.K + 511) / 512 * 512;
     auto load = [&](int r, int k) {
-        return n0 + r < m.N && k < k16 ? ld_nc_v4(m.wq + (size_t)(n0 + r) * m.ldw + k) : make_uint4(0u, 0u, 0u, 0u);
+        return n0 + r < m.N && k < k16 ? ld_v4(m.wq + (size_t)(n0 + r) * m.ldw + k) : make_uint4(0u, 0u, 0u, 0u);
     };
     uint4 w[R][kAhead];
 #pragma unroll

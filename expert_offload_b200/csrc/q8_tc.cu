@@ -396,10 +396,10 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
             const int tv = min(BT, m.T - t0);
             // the scales, while the MMAs still run
             float *xs = xs_of[warp - 2];
-            const float ws = a.split == 1 && n < m.N ? __ldg(m.ws + n) : 0.0f;
+            const float ws = a.split == 1 && n < m.N ? m.ws[n] : 0.0f;
             if (!FUSED && a.split == 1)
 #pragma unroll
-                for (int j = 0; j < BT; j += 32) xs[j + lane] = j + lane < tv ? __ldg(m.xs + t0 + j + lane) : 0.0f;
+                for (int j = 0; j < BT; j += 32) xs[j + lane] = j + lane < tv ? m.xs[t0 + j + lane] : 0.0f;
             const bool ok = wait_bar(&done, 0u, a.timeout_ns, abortp);
             __syncwarp();
             tc_fence_after_sync();
@@ -441,8 +441,8 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
         // the scales of this CTA's outputs, beside the others' last sums
         const int own = kCh / a.split, tv = min(BT, m.T - t0);
         for (int i = threadIdx.x; i < own + (FUSED ? 0 : tv); i += C::kThr) {
-            if (i < own) ws_own[i] = n0 + rank * own + i < m.N ? __ldg(m.ws + n0 + rank * own + i) : 0.0f;
-            else xs_own[i - own] = __ldg(m.xs + t0 + i - own);
+            if (i < own) ws_own[i] = n0 + rank * own + i < m.N ? m.ws[n0 + rank * own + i] : 0.0f;
+            else xs_own[i - own] = m.xs[t0 + i - own];
         }
         __syncwarp();
         cluster_sync();
@@ -651,13 +651,13 @@ q8_pair_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
             tile_of(i, ct, tt, c, t);
             const int b = n & 1, nn = c * 2 * kCh + rank * kCh + ch, t0 = t * BT;
             // the scales of the part's tokens, while the MMAs still run
-            const float ws = nn < m.N ? __ldg(m.ws + nn) : 0.0f;
+            const float ws = nn < m.N ? m.ws[nn] : 0.0f;
             float *xs = xs_of[warp - 2];
             __syncwarp();                                    // the last tile's have been read
 #pragma unroll
             for (int j = 0; j < kPart; j += 32) {
                 const int at = t0 + part * kPart + j + lane;
-                xs[j + lane] = at < m.T ? __ldg(m.xs + at) : 0.0f;
+                xs[j + lane] = at < m.T ? m.xs[at] : 0.0f;
             }
             __syncwarp();
             if (!wait_bar(&tfull[b], (uint32_t)(n / 2) & 1u, a.timeout_ns, abortp)) break;

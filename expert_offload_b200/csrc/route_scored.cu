@@ -473,12 +473,12 @@ __device__ __forceinline__ void read_bias(const Args &a, int e0, int n, float (&
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i < n) v = __ldg(reinterpret_cast<const float4 *>(a.bias + e0 + i));
+            if (i < n) v = *reinterpret_cast<const float4 *>(a.bias + e0 + i);
             b[i] = v.x, b[i + 1] = v.y, b[i + 2] = v.z, b[i + 3] = v.w;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) b[i] = a.bias && i < n ? __ldg(a.bias + e0 + i) : 0.0f;
+        for (int i = 0; i < N; ++i) b[i] = a.bias && i < n ? a.bias[e0 + i] : 0.0f;
     }
 }
 
