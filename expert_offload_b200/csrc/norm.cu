@@ -285,22 +285,32 @@ __device__ __forceinline__ void do_row(const Args &a, const Row<VEC, NV> &row, c
                 b[c][i] = R::template value<YB>(ry[c], i);
                 if (a.y2) b[c][i] = fmaf(g2, R::template value<YB>(ry2[c], i), b[c][i]);
             }
-        // what is one number for the row is multiplied once
-        float scale = a.beta;
-        if (a.gate_kind == HFQ_GATE_TOKEN) scale *= a.gate_sigmoid ? sigmoid(tg.gate) : tg.gate;
+        // What is one number for the row: its norm r, and the branch scale with the
+        // token's gate, g = m late with late a power of two and m below 2 (g without a
+        // norm keeps both).  r, m and late may leave the f32 range together where the
+        // branch does not, so the elements meet r m first (b r is at most sqrt(H)), and
+        // late comes with the weights, for which it costs nothing: late (w + offset) is
+        // one fused operation, exact but for its rounding.
+        float g = a.beta;
+        if (a.gate_kind == HFQ_GATE_TOKEN) g *= a.gate_sigmoid ? sigmoid(tg.gate) : tg.gate;
+        const uint32_t e = min(max((__float_as_uint(g) >> 23) & 0xffu, 1u), 253u);
+        const float late = __uint_as_float(e << 23);
+        float s = g * __uint_as_float((254u - e) << 23);
         if (a.w_post) {
-            scale *= red.template inv_rms<NV>(0, b, a.inv_h, a.eps);
+            s *= red.template inv_rms<NV>(0, b, a.inv_h, a.eps);
+            const float offset = a.w_offset * late;
             float w[NV][8];
             row.load_weights(a.w_post, a.w_bf16, w);
 #pragma unroll
             for (int c = 0; c < NV; ++c)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) b[c][i] *= scale * (w[c][i] + a.w_offset);
+                for (int i = 0; i < 8; ++i) b[c][i] = b[c][i] * s * fmaf(w[c][i], late, offset);
         } else {
+            s *= late;
 #pragma unroll
             for (int c = 0; c < NV; ++c)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) b[c][i] *= scale;
+                for (int i = 0; i < 8; ++i) b[c][i] *= s;
         }
         if (a.gate_kind == HFQ_GATE_FULL) multiply_gate<NV>(rg, a.gate_sigmoid, b);
         else if (a.gate_kind == HFQ_GATE_CHANNEL) {
@@ -329,7 +339,7 @@ __device__ __forceinline__ void do_row(const Args &a, const Row<VEC, NV> &row, c
 #pragma unroll
         for (int c = 0; c < NV; ++c)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[c][i] *= r * (w[c][i] + a.w_offset);
+            for (int i = 0; i < 8; ++i) x[c][i] = x[c][i] * r * (w[c][i] + a.w_offset);
     } else {
 #pragma unroll
         for (int c = 0; c < NV; ++c)

@@ -238,7 +238,9 @@ hfq_status moe_route_scored(const void *logits, hfq_dtype logits_dtype, int ld, 
  *   count), the plain norm before the first block.
  *   x' is rounded to x's type before it is normed, so that xn is the norm of
  *   what x_out holds.  All arithmetic is f32 (a row whose squares leave the
- *   f32 range is summed again at another scale); one rounding per output.  NaN
+ *   f32 range is summed again at another scale), an element's factors in this
+ *   order: its norm; the weight, together with branch_scale * act(gate) of a
+ *   token's gate; a channel's or an element's gate.  One rounding per output.  NaN
  *   and infinities of a row stay in that row.
  *   x:       [T][H] in x_dtype, rows ldx elements apart (0 = H).
  *   y, y2:   [T][H] in y_dtype, rows ldy elements apart (0 = H).
