@@ -91,6 +91,10 @@ __device__ __forceinline__ void st_async(uint32_t addr, uint32_t v, uint32_t bar
                  : "memory");
 }
 
+// Waits for copies, MMAs and stores on their way, which end by themselves: not
+// cut short by an abort, and with a limit that does not shrink with the caller's.
+constexpr long long kLandNs = 1000000000LL;
+
 struct Args {
     Q8Mat m;
     const void *x;                        // fused: the tokens as they are, rows ldx elements apart
@@ -119,6 +123,11 @@ __device__ bool wait_bar(uint64_t *bar, uint32_t parity, long long timeout_ns, v
             return false;
         }
     }
+}
+
+__device__ __forceinline__ bool wait_landed(uint64_t *bar, uint32_t parity, const Args &a)
+{
+    return wait_bar(bar, parity, a.timeout_ns + kLandNs, nullptr);
 }
 
 // 32 consecutive columns of this thread's tensor-memory lane; they are there
@@ -308,9 +317,10 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
                 if (!FUSED) tma_load_2d(dst + C::kA, &xmap, (c0 + issued) * kKb, t0, &full[s]);
                 if (++s == stages) s = 0, ++round;
             }
-            // every copy has landed before the CTA may end
+            // every copy has landed before the CTA may end, and the other CTAs' maxima
             for (int i = max(0, issued - stages); i < issued; ++i)
-                wait_bar(&full[i % stages], (uint32_t)(i / stages) & 1u, a.timeout_ns, nullptr);
+                wait_landed(&full[i % stages], (uint32_t)(i / stages) & 1u, a);
+            if (FUSED && a.split > 1) wait_landed(&amax_bar, 0u, a);
         }
         __syncwarp();
         if (a.split > 1) cluster_wait();
@@ -330,7 +340,7 @@ q8_tile_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
                 if (++s == stages) s = 0, ++round;
             }
             umma_commit(&done);
-            wait_bar(&done, 0u, a.timeout_ns, nullptr);      // after an abort, too, no MMA may still run
+            wait_landed(&done, 0u, a);                       // after an abort, too, no MMA may still run
         }
         __syncwarp();
         if (a.split > 1) cluster_wait();
@@ -536,6 +546,12 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const void *map, int
         : "memory");
 }
 
+// Takes `bytes` off what the current phase of `bar` still expects.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t bar)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -557,7 +573,8 @@ q8_pair_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
     constexpr int BT = C::kBT;
     extern __shared__ uint8_t raw[];
     uint8_t *buf = reinterpret_cast<uint8_t *>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], never;
+    __shared__ uint64_t full[C::kStages], empty[C::kStages], tfull[2], tempty[2], never, told;
+    __shared__ uint32_t peer_stages;                     // the leader's: stages that the other CTA has filled, ...
     __shared__ __align__(16) float xs_of[kEpiWarps][C::kBT / kEpiParts];
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -577,7 +594,9 @@ q8_pair_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
             mbar_init(&tempty[i], 2 * kEpiWarps);
         }
         mbar_init(&never, 1);
+        mbar_init(&told, 1);
         fence_mbar_init();
+        if (rank == 0) mbar_arrive_expect_tx(&told, 4);  // ... there once `told` has its 4 bytes
         abort_flag = 0;
     }
     if (warp == 1) {
@@ -613,10 +632,23 @@ q8_pair_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
                 tma_load_2d_pair(dst + C::kA, &xmap, k * kKb, t0, bar);
             }
         }
-        // the copies of this CTA have landed once the MMAs that read them are
-        // done; after an abort the waits that ran out gave them their time
+        // The copies of both CTAs have landed once the MMAs that read them are done.
+        // After an abort the leader, on whose barriers they count, waits for those that
+        // nobody will read; the other CTA stays until it has (the cluster's barrier).
+        if (rank == 1) st_async(map_rank(smem_u32(&peer_stages), 0), (uint32_t)g, map_rank(smem_u32(&told), 0));
+        bool read = true;
         for (int j = max(0, g - C::kStages); j < g; ++j)
-            wait_bar(&empty[j % C::kStages], (uint32_t)(j / C::kStages) & 1u, a.timeout_ns, abortp);
+            read = read && wait_bar(&empty[j % C::kStages], (uint32_t)(j / C::kStages) & 1u, a.timeout_ns, abortp);
+        if (rank == 0) {
+            const int p = wait_landed(&told, 0u, a) ? (int)peer_stages : g, both = max(g, p);
+            if (!read || *abortp) {
+                // stages that only one CTA has filled await that one's bytes
+                for (int j = g; j < p; ++j) mbar_arrive_expect_tx(&full[j % C::kStages], C::kStage);
+                for (int j = p; j < g; ++j) mbar_complete_tx(&full[j % C::kStages], C::kStage);
+                for (int j = max(0, both - C::kStages); j < both; ++j)
+                    wait_landed(&full[j % C::kStages], (uint32_t)(j / C::kStages) & 1u, a);
+            }
+        }
     } else if (warp == 1 && lane == 0 && rank == 0) {
         bool ok = !a.hook || wait_bar(&never, 0u, a.timeout_ns, abortp);
         int g = 0, n = 0;
@@ -638,7 +670,7 @@ q8_pair_kernel(const Args a, const __grid_constant__ CUtensorMap wmap, const __g
             umma_commit_pair(&tfull[b]);
         }
         // no MMA may run when the pair ends: its last commit has arrived
-        if (n > 0) wait_bar(&tfull[(n - 1) & 1], (uint32_t)((n - 1) / 2) & 1u, a.timeout_ns, nullptr);
+        if (n > 0) wait_landed(&tfull[(n - 1) & 1], (uint32_t)((n - 1) / 2) & 1u, a);
     } else if (warp >= 2) {
         // the sums: warp w reads lanes 32 (w % 4) .. + 31, one part of the columns
         constexpr int kPart = BT / kEpiParts;
