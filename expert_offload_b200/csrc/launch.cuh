@@ -28,6 +28,14 @@ __device__ __forceinline__ void begin_ordered()
     let_next_begin();
 }
 
+// The result of a runtime call, which its caller reports: the runtime keeps the
+// error, too, and the next call's check of its own launch would find it there.
+inline cudaError_t reported(cudaError_t e)
+{
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+
 template <class... P, class... A>
 cudaError_t launch_ordered(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A &...args)
 {
@@ -41,7 +49,7 @@ cudaError_t launch_ordered(void (*kernel)(P...), dim3 grid, dim3 block, size_t s
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    return reported(cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...));
 }
 
 }  // namespace hfq

@@ -63,7 +63,7 @@ hfq_status take_status(void *word_dev, const char *who, cudaStream_t s)
         e = cudaMemsetAsync(word_dev, 0, sizeof word, s);
         if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     }
-    if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
+    if (reported(e) != cudaSuccess) return fail(HFQ_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
     if (word) return fail((hfq_status)(int)word, "a device-side wait of %s ran out (status %d)", who, (int)word);
     return ok();
 }

@@ -3,6 +3,7 @@
 
 #include <atomic>
 
+#include "launch.cuh"
 #include "quant8.cuh"
 
 namespace hfq {
@@ -31,11 +32,11 @@ hfq_status launch_q8_fused(const Q8Mat &a, const void *x, bool x_bf16, size_t ld
 inline cudaError_t allow_smem(const void *f, int bytes, std::atomic<unsigned long long> &done)
 {
     int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = reported(cudaGetDevice(&dev));
     if (e != cudaSuccess) return e;
     const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
     if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    e = reported(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
     if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
     return e;
 }

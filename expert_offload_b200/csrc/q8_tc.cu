@@ -732,7 +732,7 @@ EncodeTiled encode_fn()
     static const EncodeTiled fn = [] {
         void *p = nullptr;
         cudaDriverEntryPointQueryResult q;
-        const bool found = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        const bool found = reported(cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q)) == cudaSuccess &&
                            q == cudaDriverEntryPointSuccess;
         return found ? reinterpret_cast<EncodeTiled>(p) : nullptr;
     }();
@@ -778,7 +778,7 @@ cudaError_t launch_tile(Args a, const CUtensorMap &wmap, const CUtensorMap &xmap
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, q8_tile_kernel<BT, MODE>, a, wmap, xmap);
+    return reported(cudaLaunchKernelEx(&cfg, q8_tile_kernel<BT, MODE>, a, wmap, xmap));
 }
 
 cudaError_t launch_pair(const Args &a, const CUtensorMap &wmap, const CUtensorMap &xmap, cudaStream_t s)
@@ -829,7 +829,6 @@ hfq_status launch_q8_fused(const Q8Mat &m, const void *x, bool x_bf16, size_t ld
     if (!encode(&wmap, m.wq, m.K, m.N, m.ldw, kCh))
         return fail(HFQ_ERR_CUDA, "8-bit product: tensor map encoding failed (K %d, N %d)", m.K, m.N);
     cudaError_t e = x_bf16 ? launch_tile<kFew, kFusedBf16>(a, wmap, wmap, s) : launch_tile<kFew, kFusedF32>(a, wmap, wmap, s);
-    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "8-bit product launch: %s", cudaGetErrorString(e));
     return HFQ_OK;
 }
@@ -863,7 +862,6 @@ hfq_status launch_q8_tc(const Q8Mat &m, bool chained, cudaStream_t s)
                     : bt == 32 ? launch_tile<32, kPlain>(a, wmap, xmap, s)
                     : bt == 64 ? launch_tile<64, kPlain>(a, wmap, xmap, s)
                                : launch_tile<128, kPlain>(a, wmap, xmap, s);
-    if (e == cudaSuccess) e = cudaGetLastError();
     if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "8-bit product launch: %s", cudaGetErrorString(e));
     return HFQ_OK;
 }
@@ -871,7 +869,7 @@ hfq_status launch_q8_tc(const Q8Mat &m, bool chained, cudaStream_t s)
 hfq_status q8_status(cudaStream_t s)
 {
     void *p = nullptr;
-    const cudaError_t e = cudaGetSymbolAddress(&p, g_status);
+    const cudaError_t e = reported(cudaGetSymbolAddress(&p, g_status));
     if (e != cudaSuccess) return fail(HFQ_ERR_CUDA, "status read: %s", cudaGetErrorString(e));
     return take_status(p, "an 8-bit product", s);
 }
