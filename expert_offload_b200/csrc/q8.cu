@@ -106,33 +106,40 @@ __global__ void __launch_bounds__(512, SWIGLU && NV > 2 ? 1 : 2) quantize_vec_ke
     if (j == 0) a.scale[r] = row_scale(top);
 }
 
-// Rows of any length and alignment: neighbouring threads read neighbouring
-// elements, and the bytes change places in shared memory.  517 rows of 2001 in
-// f32 take 2.8 us (3.6 with threads of eight neighbours each), 8192 of 8001 66.6
-// (73.2); in bf16 2.5 (2.8) and, bound by their 2-byte loads, 91.8 (84.1).
+// Rows of any length and alignment.  Of f32, neighbouring threads read
+// neighbouring elements, and the bytes change places in shared memory: 517 rows
+// of 2001 take 2.6 us (3.1 with threads of eight neighbours each), 8192 of 8001
+// 66.3 (70.4), with SwiGLU 131 (141).  Of bf16, whose single elements are half as
+// wide, a thread reads eight neighbours, mostly from L1, and writes their bytes
+// itself: 8192 rows of 2001 take 18.7 us (22.8 the other way), of 8001 73.6
+// (91.5), with SwiGLU 137 (187); 517 of 8001 5.9 (5.7).
 template <int NV, bool BF16, bool SWIGLU>
 __global__ void __launch_bounds__(512) quantize_kernel(QuantArgs a)
 {
+    constexpr bool EIGHT = BF16;
     __shared__ uint32_t red[16];
-    __shared__ __align__(16) uint8_t bytes[512 * NV * 8];
+    __shared__ __align__(16) uint8_t bytes[EIGHT ? 16 : 512 * NV * 8];
     begin_ordered();
     const int sub = threadIdx.x / a.per_row, j = threadIdx.x & (a.per_row - 1);
     const size_t r = (size_t)blockIdx.x * (blockDim.x / a.per_row) + sub;
     const bool in = r < (size_t)a.rows;
     const void *row = row_at(a.x, BF16, in ? r * a.ldx : 0);
     const int n = in ? a.cols : 0;
-    auto read = [&](int c) { return c < n ? load_act(row, BF16 ? HFQ_BF16 : HFQ_F32, c) : 0.0f; };
+    auto read = [&](int i, int e) {
+        const int c = EIGHT ? (i * a.per_row + j) * 8 + e : (i * 8 + e) * a.per_row + j;
+        return c < n ? load_act(row, BF16 ? HFQ_BF16 : HFQ_F32, c) : 0.0f;
+    };
     float v[NV][8], u[SWIGLU ? NV : 1][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[i][e] = read((i * 8 + e) * a.per_row + j);
+        for (int e = 0; e < 8; ++e) v[i][e] = read(i, e);
     if (SWIGLU) {
         row = row_at(row, BF16, a.cols);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) u[i][e] = read((i * 8 + e) * a.per_row + j);
+            for (int e = 0; e < 8; ++e) u[i][e] = read(i, e);
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -145,17 +152,25 @@ __global__ void __launch_bounds__(512) quantize_kernel(QuantArgs a)
         for (int e = 0; e < 8; ++e) top = max(top, abs_bits(v[i][e]));
     top = row_top(a, top, red);
     const RowQuant<BF16 && !SWIGLU> q(top);
-    uint8_t *mine = bytes + sub * a.per_row * NV * 8;
+    if (EIGHT) {
+        if (!in) return;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const uint2 b = q(v[i]);
+        for (int i = 0; i < NV; ++i) write_row(a, r, j, i, q(v[i]));
+    } else {
+        uint8_t *mine = bytes + sub * a.per_row * NV * 8;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mine[(i * 8 + e) * a.per_row + j] = (uint8_t)((e < 4 ? b.x : b.y) >> 8 * (e & 3));
+        for (int i = 0; i < NV; ++i) {
+            const uint2 b = q(v[i]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                mine[(i * 8 + e) * a.per_row + j] = (uint8_t)((e < 4 ? b.x : b.y) >> 8 * (e & 3));
+        }
+        __syncthreads();
+        if (!in) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            write_row(a, r, j, i, *reinterpret_cast<const uint2 *>(mine + (i * a.per_row + j) * 8));
     }
-    __syncthreads();
-    if (!in) return;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) write_row(a, r, j, i, *reinterpret_cast<const uint2 *>(mine + (i * a.per_row + j) * 8));
     if (j == 0) a.scale[r] = row_scale(top);
 }
 
