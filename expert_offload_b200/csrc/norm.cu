@@ -4,8 +4,9 @@
 // One block of threads holds a row in registers from its first read to its
 // last write: y, y2, x and the gate are read once, x' and xn written once, and
 // the two (three with the 8-bit output) reductions over the row go through
-// shared memory.  Bound by memory: at a bf16 stream and an f32 block output 20
-// bytes an element, so what counts is how many bytes are on their way.
+// shared memory.  Bound by memory: at a bf16 stream and an f32 block output 10
+// bytes an element, with a second branch 14, so what counts is how many bytes
+// are on their way.
 //
 // Everything a row needs is requested before anything is used, so that a row
 // costs one trip to memory.
@@ -165,8 +166,8 @@ struct Row {
 };
 
 // Reductions over the block in a fixed order; every thread gets the result.
-// Each has words of its own for even and odd rows, so one barrier is enough:
-// a thread that is a barrier ahead writes words that nobody reads any more.
+// Each of a row's five has words of its own, so one barrier is enough: a thread
+// that is a barrier ahead writes words that nobody has read or reads any more.
 constexpr int kReds = 5;
 constexpr int kMaxWarps = 16;
 
@@ -378,12 +379,16 @@ __device__ __forceinline__ void do_row(const Args &a, const Row<VEC, NV> &row, c
 }
 
 // Registers are held down for the sake of rows at work: 8192 rows of 2048 (bf16
-// stream, two f32 branches, 235 MB) take 40.8 us with five blocks of 256 threads
+// stream, two f32 branches, 235 MB) take 39.3 us with five blocks of 256 threads
 // on an SM, 44 with four, 50.6 with the weights held in registers from the start;
-// 2048 rows of 8192 with a full gate (201 MB) take 45.5 us with two blocks of
+// 2048 rows of 8192 with a full gate (201 MB) take 40.4 us with two blocks of
 // 512 and 61.9 with one.  A ring of rows in shared memory, filled by bulk copies
 // ahead of persistent blocks, was slower (52 and 72 us): what a row waits for is
 // its two reductions, and more rows at once hide those best.
+// The 64 registers that two blocks of 512 leave a thread do not hold all operands
+// that a call may have: rows above 2048 spill, 68 to 300 bytes a thread (bf16 to
+// f32) where they are whole chunks, 332 to 492 where they are not (2048 rows of
+// 8191 with a full gate: 107.7 us); the 48 of shorter rows spill 20.
 template <bool VEC, int NV, bool XB, bool YB>
 __global__ void __launch_bounds__(NV * 256, NV > 1 ? 2 : VEC ? 5 : 3) norm_kernel(const Args a)
 {

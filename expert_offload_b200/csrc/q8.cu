@@ -373,10 +373,14 @@ bool takes_dot(int T, int K, int N)
 
 // Up to eight tokens and few weights: the fused kernel, one launch (and 2 us of
 // host time) less.  With more weights the quantiser's own kernel, beside which
-// the product starts its weights, is quicker on the GPU (16.9 against 19.0 us for
-// 5 tokens of 8192 x 8192; 7.0 against 6.9 of 2048 x 8192), and with long rows,
-// which one warp a token quantises slowly (8192 x 2048: 7.5 against 8.3, 16384 x
-// 1024: 10.1 and 11.7; 4096 x 4096: 7.4 both; 2000 x 4096: 6.8 and 5.9).
+// the product starts its weights, is as quick on the GPU and then quicker, and
+// with long rows, which one warp a token quantises slowly.  The two ways in us, 5
+// tokens, quantiser and product against fused: 2048 x 6144 6.6 and 6.1, x 8192 7.1
+// and 6.7, x 9216 9.8 and 11.1, x 12288 8.5 and 8.6, x 16384 9.4 and 9.5, x 24576
+// 13.5 and 14.9; 1024 x 16384 7.4 and 6.9, x 32768 9.3 and 8.3; 512 x 32768 6.3
+// and 5.8, x 65536 10.0 and 11.3; 4096 x 2048 6.0 and 5.8, x 4096 7.2 and 8.0, x
+// 6144 8.1 and 8.6; 8192 x 2048 7.5 and 8.3; 16384 x 1024 10.1 and 11.7.  So they
+// meet between 16 MB and 32 MB of weights, at 4096 before that.
 bool takes_fused(int T, int K, int N) { return T <= kQ8FusedTokens && K <= 4096 && (long long)K * N <= (16 << 20); }
 
 hfq_status run_dot(const DotArgs &a, cudaStream_t s)

@@ -102,7 +102,7 @@ struct Args {
     int x_vec;
     long long timeout_ns;
     int stages;                           // of the tile kernel's ring
-    int split;                            // CTAs of a cluster, each with a share of K (two stages at least)
+    int split;                            // CTAs of a cluster, each with a share of K (two stages at least, of 16-token tiles one)
     int share;                            // stages of K that a CTA of the cluster takes at most
     int chained;                          // launched behind the quantiser, beside which it may start
     int hook;                             // test hook: the MMA warp waits for an arrival that never comes
@@ -229,7 +229,8 @@ __device__ __forceinline__ void store_columns(const Q8Mat &m, int t0, int n, int
 // cluster), and write the CTA's share of the quantised rows where the MMAs read
 // them, in the 128-byte swizzle that a TMA load would have given them.  One
 // launch; x is read from L2 by every channel tile.  5 tokens of 2048 x 1024 take
-// 4.5 us, of 2048 x 8192 (17 MB of weights, 2.6 us) 6.7.
+// 4.4 us, of 2048 x 8192 (17 MB of weights, 2.6 us at HBM's rate) 6.7 where the
+// weights lie in L2 and 7.9 where each call finds its own in HBM.
 constexpr int kFew = 16;                  // tokens of its tile
 constexpr int kQuantWarps = 8;
 

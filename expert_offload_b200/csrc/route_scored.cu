@@ -15,12 +15,22 @@
 // If two candidates lie within their errors of each other the lanes take their
 // candidates' scores again in 64 bits and rank those; the groups' standing is
 // settled the same way from each group's two best.  Where there are more than
-// 32 candidates (many equal scores) or fewer than k live experts the token is
-// decided in 64 bits from the start (select64).
-// Without a bias the logits decide, which are exact as they are.
+// 32 candidates or fewer than k live experts the token is decided in 64 bits
+// from the start (select64).  Without a bias the logits decide, which are exact
+// as they are.
 //
-// Bound by instructions: a token of 512 experts in 8 groups is 1170 of a warp,
-// with its pairs counted (8192 tokens: 14.4 us without lists, 26.4 with them).
+// More than 32 candidates come from equal scores, and from rules that leave few
+// lanes for k experts, since a lane counts with its best alone and lanes of
+// dropped groups not at all.  Of normal logits with sigmoid scores and a bias, 512
+// experts: 4 of 8 groups leave none to select64 at k = 8, a fifth of the tokens at
+// k = 14, seven of eight at k = 16; 1 of 8, 2 of 16 or 4 of 32 groups all, at k = 8
+// (their live lanes are fewer than k).  8192 tokens then take 17.8 us, 82, 121,
+// and 88 to 94; one token 4.3 and, decided in 64 bits, 17.6.
+//
+// Bound by chains of dependent steps, with the registers for 16 warps an SM: a
+// token of 512 experts in 8 groups is 1170 instructions of a warp, with its pairs
+// counted, and half of the issue slots are used (8192 tokens: 17.8 us without
+// lists, 26 to 28 with them; of one group 14.3 and 22.9).
 #include <algorithm>
 #include <cfloat>
 
@@ -314,12 +324,15 @@ __device__ __forceinline__ Slot select_token(const Args &a, size_t row, const fl
     const int grp = lane / a.tpl, part = lane - grp * a.tpl;
     const int e0 = grp * a.size + part * a.run;
     const bool scored = a.bias || (a.n_groups > 1 && a.group_top > 1);
-    // Errors, in units of 2^-24.  An exponential is off by 4, and by 1.5 for each
-    // unit of its argument (rounding of the product, of the constant).  Sigmoid:
-    // that counts s (1 - s) times, under 1.4 in all; sum 1, reciprocal 2: under 8.
-    // Softmax: numerator 4 (far ones are small), sum 4 + 1.5 times the mean
-    // distance (at most ln 512) + 35 additions, quotient 3: under 64 of the
-    // largest score, 1 / z.  The bias' addition: |c|.
+    // Errors, in units of 2^-24.  An exponential is off by 4 (its unit, 2^-22), and
+    // by 1.3 for each unit of its argument (the rounding of the product, and of the
+    // constant, 0.3).  Sigmoid: that counts s (1 - s) times, under 1.4 in all; sum
+    // 1, reciprocal 2: under 8.  Softmax: the argument l - m is rounded, too, 2.3 for
+    // each unit.  Numerator 4, relative to the largest score ((4 + 2.3 d) exp(-d) is
+    // largest at a distance of 0); sum 4 + 2.3 times the mean distance, which is at
+    // most ln 512 = 6.24, + 34 additions (30 of a lane, then 5); reciprocal and
+    // product 3: 60 in all, under 64, of the largest score, 1 / z.  The bias'
+    // addition: |c|.
     const float smax = a.sigmoid ? 1.0f : rcp_approx(z), base = kU * (a.sigmoid ? 8.0f : 64.0f * smax);
     float c[N];                  // what experts are compared by
     bool keep = grp < a.n_groups;

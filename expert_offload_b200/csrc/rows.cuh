@@ -35,9 +35,6 @@ __device__ __forceinline__ void expand8(const Raw8 &r, float (&v)[8])
         v[i] = BF16 ? __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16) : __uint_as_float(w[i]);
 }
 
-// Rounds v to bf16 (as a float).
-__device__ __forceinline__ float round_bf16(float v) { return bf16_bits_to_float(float_to_bf16_bits(v)); }
-
 // The largest magnitude of eight elements, as f32 bits.
 template <bool BF16>
 __device__ __forceinline__ uint32_t raw_max(const Raw8 &r)
