@@ -26,7 +26,7 @@
 #define MAX_KINDS 8
 
 static PyObject *g_error, *g_tensor, *g_get_device, *g_layout, *g_kinds[MAX_KINDS];
-static PyObject *s_dtype, *s_get_device, *s_is_contiguous, *s_numel, *s_data_ptr;
+static PyObject *s_shape, *s_dtype, *s_get_device, *s_is_contiguous, *s_numel, *s_data_ptr;
 
 typedef int64_t V;
 #define P(i) ((void *)(uintptr_t)v[i])
@@ -162,12 +162,24 @@ static int operand(PyObject *op, V *v, V *device)
         if (!is_dense) return fail_arg(name, "has gaps between its elements, which the call takes as neighbours");
         if (rows > 0 && cols > 0 && numel < rows * cols)
             return fail_arg(name, "holds fewer elements than the call reads or writes");
-    } else if (rows > 0 && cols > 0 && ld >= cols &&     /* else the library refuses the sizes */
-               !(is_dense && numel == rows * ld && whole <= ld)) {
-        PyObject *r = PyObject_CallFunction(g_layout, "OOLLLL", name, t, (long long)rows, (long long)cols, (long long)ld,
-                                            (long long)whole);
-        if (!r) return -1;
-        Py_DECREF(r);
+    } else if (rows > 0 && cols > 0 && ld >= cols) {     /* else the library refuses the sizes */
+        int plain = is_dense && numel == rows * ld && whole <= ld;
+        if (!plain && is_dense && numel >= (rows - 1) * ld + whole) {
+            PyObject *shape = PyObject_GetAttr(t, s_shape);
+            if (!shape) return -1;
+            const Py_ssize_t n = PyTuple_Check(shape) ? PyTuple_GET_SIZE(shape) : 0;
+            V last = 0;
+            const int st = n > 0 ? to_word(PyTuple_GET_ITEM(shape, n - 1), &last) : 0;
+            Py_DECREF(shape);
+            if (st) return -1;
+            plain = n == 1 || last == ld;                /* a flat buffer, or rows of ld elements */
+        }
+        if (!plain) {
+            PyObject *r = PyObject_CallFunction(g_layout, "OOLLLL", name, t, (long long)rows, (long long)cols,
+                                                (long long)ld, (long long)whole);
+            if (!r) return -1;
+            Py_DECREF(r);
+        }
     }
     return ask(t, s_data_ptr, v);
 }
@@ -255,6 +267,7 @@ PyMODINIT_FUNC PyInit__bind(void)
     s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
     s_numel = PyUnicode_InternFromString("numel");
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
-    if (!s_dtype || !s_get_device || !s_is_contiguous || !s_numel || !s_data_ptr) return NULL;
+    s_shape = PyUnicode_InternFromString("shape");
+    if (!s_shape || !s_dtype || !s_get_device || !s_is_contiguous || !s_numel || !s_data_ptr) return NULL;
     return PyModule_Create(&module);
 }

@@ -122,6 +122,12 @@ def test_rows_lie_as_far_apart_as_the_call_says():
     _passes(_quantise(x=wide[:, 136:], ldx=200))
     _passes(_quantise(x=wide, ldx=200))
     _passes(_quantise(x=wide[:1, :64], rows=1))
+    _passes(_quantise(x=_t(40, 64)))                     # buffers for more rows than the call has
+    _passes(_quantise(x=_t(40, 64), rows=1))
+    _passes(_quantise(x=_t(40, 4, 16)))
+    _passes(_quantise(x=_t(6, 5, 64)))
+    _refused(_quantise(x=_t(64, 40)), "x")               # as many elements in other rows
+    _refused(_quantise(x=_t(8, 128)), "x")
     _passes(_quantise(x=_t(4, 4, 16)))                   # heads side by side: one row
     _passes(_quantise(x=_t(2, 2, 64)))                   # two dimensions of rows
     _passes(_quantise(x=_t(2, 2, 100)[:, :, :64], ldx=100))
